@@ -21,13 +21,16 @@ LIB_PATH = os.path.join(_HERE, "libnvfp4.so")
 
 # status codes, enumerations (values of include/nvfp4.h)
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_DTYPE, ERR_WORKSPACE, ERR_ARCH, ERR_LAUNCH, ERR_LAYOUT, ERR_MODE, \
-    ERR_DEVICE_TIMEOUT = range(11)
+    ERR_DEVICE_TIMEOUT, ERR_PAGE = range(12)
 DTYPE_F32, DTYPE_BF16 = 0, 1
 SF_ROWMAJOR, SF_TILED = 0, 1
 MODE_AUTO, MODE_W4A16, MODE_W4A4 = 0, 1, 2
 EPI_NONE, EPI_SWIGLU, EPI_COMBINE = 0, 1, 2
 
 
+KV_BF16, KV_E4M3, KV_NVFP4 = 0, 1, 2
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_YARN = 0, 1, 2, 3
 CHAIN_SRC_X, CHAIN_SRC_OP = 0, 1
 CHAIN_XFORM_NONE, CHAIN_XFORM_RMS, CHAIN_XFORM_SILU_MUL = 0, 1, 2
 
@@ -39,6 +42,13 @@ class ChainOp(ctypes.Structure):
                 ("x", ctypes.c_void_p), ("x_ld", ctypes.c_int64), ("xform", ctypes.c_int32),
                 ("y_xform", ctypes.c_int32), ("y", ctypes.c_void_p), ("y_dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class KvCacheDesc(ctypes.Structure):
+    """``nvfp4_kv_cache`` of include/nvfp4.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("k_gs", ctypes.c_void_p), ("v_gs", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
 
 
 class NVFP4Error(RuntimeError):
@@ -59,6 +69,7 @@ def lib() -> ctypes.CDLL:
                               "(there is no fallback implementation)")
         L = ctypes.CDLL(LIB_PATH)
         p, i64, i32, sz, i = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int
+        f32, f64 = ctypes.c_float, ctypes.c_double
         sig = {
             "nvfp4_status_string": (ctypes.c_char_p, [i]),
             "nvfp4_version": (i, []),
@@ -78,6 +89,14 @@ def lib() -> ctypes.CDLL:
             "nvfp4_silu_mul": (i, [p, i, i64, i64, p, p]),
             "nvfp4_rms_norm_quant_workspace": (sz, [i64]),
             "nvfp4_rms_norm_quant": (i, [p, i, i64, i64, i64, i, p, p, p, p, sz, p]),
+            "nvfp4_rope_freqs": (i, [i32, f64, i, f64, f64, f64, f64, p, p]),
+            "nvfp4_rope": (i, [p, i, i64, i32, i32, i64, p, p, i32, i, f32, i, p, i, i64, p]),
+            "nvfp4_kv_cache_bytes": (sz, [i64, i32, i32, i32, i]),
+            "nvfp4_kv_write": (i, [p, p, p, i, i64, i64, i64, p, p]),
+            "nvfp4_kv_read": (i, [p, p, i64, p, p, i, p]),
+            "nvfp4_rope_kv_write": (i, [p, p, p, p, i, i64, i32, i64, i64, i64, p, p, p, i32, i, f32, p, p]),
+            "nvfp4_attn_decode_workspace": (sz, [p, i64, i32, i64]),
+            "nvfp4_attn_decode": (i, [p, i64, i32, i64, p, p, i64, i64, p, f32, i32, p, i, p, p, sz, p]),
             "moe_route_topk_workspace": (sz, [i64, i32, i32]),
             "moe_route_topk": (i, [p, p, p, i64, i64, i32, i32, p, p, p, p, p, p, p, p, sz, p]),
             "moe_route_topk_noalloc": (i, [p, p, p, i64, i64, i32, i32, p, p, p, p, p, p, p, p]),
@@ -375,6 +394,209 @@ def moe_layer_decode(h: torch.Tensor, w_router: torch.Tensor, k: int, gate_up, d
                                   _ptr(ex.get("topk_w")), _ptr(ex.get("a")), _ptr(y), _dtype_code(y), _ptr(ws),
                                   wsb, _stream()), "moe_layer_decode")
     return (y, ex) if ex else y
+
+# ---- rotary positions, the paged key-value cache, attention of one new token -------
+
+
+def _launch(dev: torch.device, name: str, *args):
+    """Call a C entry point on ``dev``'s current stream (made the current device for
+    the call when it is not)."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(dev, name, *args)
+    status = getattr(_lib or lib(), name)(*args, torch.cuda.current_stream().cuda_stream)
+    if status != OK:
+        raise NVFP4Error(status, name)
+
+
+def _heads_view(t: torch.Tensor, what: str, shape=None) -> int:
+    """Row stride (elements) of a ``[rows, heads, head_dim]`` view whose heads are
+    packed, as a slice of fused QKV rows is."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{what} must be a [rows, heads, head_dim] view with packed heads")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _vector(t: torch.Tensor, dtype, n: int | None, dev, what: str) -> int:
+    """Address of a contiguous vector of ``n`` elements of ``dtype`` on ``dev``."""
+    if t.dtype != dtype or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor" + (f" of {n} elements" if n is not None else ""))
+    if t.device != dev:
+        raise ValueError(f"{what} must be on {dev}, not {t.device}")
+    return t.data_ptr()
+
+
+def _cuda(t: torch.Tensor, what: str, dev=None) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{what} must be on {dev}, not {t.device}")
+    return t.device
+
+
+class KVCache:
+    """A paged key-value cache: the device memory ``data`` (uint8, contiguous, a whole
+    number of pages) with its shape, format and the fp32 global scales of the keys
+    and values (one-element tensors; not used by ``KV_BF16``)."""
+
+    def __init__(self, data: torch.Tensor, page_size: int, heads: int, head_dim: int, format: int, k_gs=None,
+                 v_gs=None):
+        page = nvfp4_kv_cache_bytes(1, page_size, heads, head_dim, format)
+        if page == 0:
+            raise ValueError("page_size, heads, head_dim or format out of range")
+        dev = _cuda(data, "data")
+        if data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() == 0 or data.numel() % page:
+            raise ValueError(f"data must be a contiguous uint8 tensor of whole pages ({page} bytes each)")
+        if format == KV_BF16:
+            k_gs = v_gs = None
+        elif k_gs is None or v_gs is None:
+            raise ValueError("this format needs k_gs and v_gs")
+        self.data, self.k_gs, self.v_gs = data, k_gs, v_gs
+        self.num_pages, self.page_size, self.heads = data.numel() // page, int(page_size), int(heads)
+        self.head_dim, self.format, self.device = int(head_dim), int(format), dev
+        self._desc = KvCacheDesc(data.data_ptr(), None if k_gs is None else _vector(k_gs, torch.float32, 1, dev, "k_gs"),
+                                 None if v_gs is None else _vector(v_gs, torch.float32, 1, dev, "v_gs"),
+                                 self.num_pages, self.page_size, self.heads, self.head_dim, self.format)
+        self._ref = ctypes.byref(self._desc)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, heads: int, head_dim: int, format: int, k_gs=None, v_gs=None,
+              device="cuda"):
+        n = nvfp4_kv_cache_bytes(num_pages, page_size, heads, head_dim, format)
+        if n == 0:
+            raise ValueError("num_pages, page_size, heads, head_dim or format out of range")
+        return cls(torch.empty(n, dtype=torch.uint8, device=device), page_size, heads, head_dim, format, k_gs, v_gs)
+
+
+def nvfp4_kv_cache_bytes(num_pages: int, page_size: int, heads: int, head_dim: int, format: int) -> int:
+    return int(lib().nvfp4_kv_cache_bytes(num_pages, page_size, heads, head_dim, format))
+
+
+def nvfp4_rope_freqs(rot_dim: int, theta: float = 10000.0, scaling: int = ROPE_SCALE_NONE, factor: float = 1.0,
+                     original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """Rotary frequencies in turns per token (fp64, on the CPU) and the magnitude of
+    cos and sin: ``(freqs [rot_dim / 2], mscale)``."""
+    if rot_dim < 2:
+        raise NVFP4Error(ERR_SHAPE, "nvfp4_rope_freqs")
+    f = torch.empty(int(rot_dim) // 2, dtype=torch.float64)
+    m = ctypes.c_double(0.0)
+    _check(lib().nvfp4_rope_freqs(rot_dim, theta, scaling, factor, original_len, beta_fast, beta_slow, f.data_ptr(),
+                                  ctypes.byref(m)), "nvfp4_rope_freqs")
+    return f, m.value
+
+
+def nvfp4_rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, layout: int = ROPE_HALF,
+               mscale: float = 1.0, inverse: bool = False, y=None, y_dtype=torch.bfloat16):
+    """Rotary positions of ``x [T, heads, head_dim]`` (fp32 or bf16; a view of wider rows
+    is read in place).  ``positions [T]`` int64, ``freqs`` from :func:`nvfp4_rope_freqs`
+    on x's device.  ``y=x`` rotates in place."""
+    dev = _cuda(x, "x")
+    x_ld = _heads_view(x, "x")
+    T, heads, D = x.shape
+    if y is None:
+        y = torch.empty((T, heads, D), dtype=y_dtype, device=dev)
+        y_ld = heads * D
+    else:
+        _cuda(y, "y", dev)
+        y_ld = _heads_view(y, "y", x.shape)
+    _launch(dev, "nvfp4_rope", x.data_ptr(), _dtype_code(x), T, heads, D, x_ld,
+            _vector(positions, torch.int64, T, dev, "positions"), _vector(freqs, torch.float64, None, dev, "freqs"),
+            2 * freqs.numel(), layout, mscale, int(inverse), y.data_ptr(), _dtype_code(y), y_ld)
+    return y
+
+
+def nvfp4_kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor):
+    """Write token t's keys and values (``[T, heads, head_dim]`` views, fp32 or bf16) to
+    slot ``slots[t]`` (int64; page * page_size + offset; negative: skipped)."""
+    dev = cache.device
+    shape = (k.shape[0], cache.heads, cache.head_dim)
+    _cuda(k, "k", dev), _cuda(v, "v", dev)
+    k_ld, v_ld = _heads_view(k, "k", shape), _heads_view(v, "v", shape)
+    if k.dtype != v.dtype:
+        raise TypeError("k and v must have one dtype")
+    _launch(dev, "nvfp4_kv_write", cache._ref, k.data_ptr(), v.data_ptr(), _dtype_code(k), shape[0], k_ld, v_ld,
+            _vector(slots, torch.int64, shape[0], dev, "slots"))
+
+
+def nvfp4_kv_read(cache: KVCache, slots: torch.Tensor, k_out=None, v_out=None, y_dtype=torch.bfloat16):
+    """The dequantized keys and values of ``slots [T]``: two ``[T, heads, head_dim]``
+    tensors (bf16 or fp32); zeros for negative slots."""
+    dev = cache.device
+    T = slots.numel()
+    shape = (T, cache.heads, cache.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=y_dtype if v_out is None else v_out.dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=k_out.dtype, device=dev)
+    if k_out.dtype != v_out.dtype:
+        raise TypeError("k_out and v_out must have one dtype")
+    code, n = _dtype_code(k_out), T * cache.heads * cache.head_dim
+    _launch(dev, "nvfp4_kv_read", cache._ref, _vector(slots, torch.int64, T, dev, "slots"), T,
+            _vector(k_out, k_out.dtype, n, dev, "k_out"), _vector(v_out, v_out.dtype, n, dev, "v_out"), code)
+    return k_out, v_out
+
+
+def nvfp4_rope_kv_write(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                        slots: torch.Tensor, freqs: torch.Tensor, layout: int = ROPE_HALF, mscale: float = 1.0,
+                        q_out=None):
+    """Rotate queries and keys and write the rotated keys and the values to the cache in
+    one pass over the QKV rows; returns the rotated queries ``[T, q_heads, head_dim]``
+    (bf16).  Same bits as :func:`nvfp4_rope` and :func:`nvfp4_kv_write`."""
+    dev = cache.device
+    T, q_heads = q.shape[0], q.shape[1]
+    _cuda(q, "q", dev), _cuda(k, "k", dev), _cuda(v, "v", dev)
+    shape = (T, cache.heads, cache.head_dim)
+    q_ld = _heads_view(q, "q", (T, q_heads, cache.head_dim))
+    k_ld, v_ld = _heads_view(k, "k", shape), _heads_view(v, "v", shape)
+    if q.dtype != k.dtype or k.dtype != v.dtype:
+        raise TypeError("q, k and v must have one dtype")
+    if q_out is None:
+        q_out = torch.empty((T, q_heads, cache.head_dim), dtype=torch.bfloat16, device=dev)
+    _launch(dev, "nvfp4_rope_kv_write", cache._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), T,
+            q_heads, q_ld, k_ld, v_ld, _vector(positions, torch.int64, T, dev, "positions"),
+            _vector(slots, torch.int64, T, dev, "slots"), _vector(freqs, torch.float64, None, dev, "freqs"),
+            2 * freqs.numel(), layout, mscale,
+            _vector(q_out, torch.bfloat16, T * q_heads * cache.head_dim, dev, "q_out"))
+    return q_out
+
+
+def nvfp4_attn_decode_workspace(cache: KVCache, B: int, q_heads: int, max_pages: int) -> int:
+    return int(lib().nvfp4_attn_decode_workspace(cache._ref, B, q_heads, max_pages))
+
+
+def nvfp4_attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, scale=None,
+                      window: int = 0, y=None, y_dtype=torch.bfloat16, want_lse: bool = False, ws=None):
+    """Attention of one new token per sequence: ``q [B, q_heads, head_dim]`` (bf16 view)
+    over the paged cache.  ``page_table [B, max_pages]`` and ``seq_lens [B]`` int32;
+    ``scale`` defaults to ``head_dim ** -0.5``.  Returns ``y [B, q_heads, head_dim]``,
+    or ``(y, lse [B, q_heads])``."""
+    dev = cache.device
+    _cuda(q, "q", dev)
+    B, q_heads = q.shape[0], q.shape[1]
+    D = cache.head_dim
+    q_ld = _heads_view(q, "q", (B, q_heads, D))
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be bfloat16, not {q.dtype}")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
+            page_table.stride(1) != 1 or page_table.device != dev:
+        raise ValueError(f"page_table must be an int32 [{B}, max_pages] tensor on {dev} with contiguous rows")
+    max_pages = page_table.shape[1]
+    table_ld = page_table.stride(0) if B > 1 else max_pages
+    if y is None:
+        y = torch.empty((B, q_heads, D), dtype=y_dtype, device=dev)
+    y_ptr = _vector(y, y.dtype, B * q_heads * D, dev, "y")
+    lse = torch.empty((B, q_heads), dtype=torch.float32, device=dev) if want_lse else None
+    if ws is None:
+        ws = torch.empty(nvfp4_attn_decode_workspace(cache, B, q_heads, max_pages), dtype=torch.uint8, device=dev)
+    else:
+        _cuda(ws, "ws", dev)
+    _launch(dev, "nvfp4_attn_decode", q.data_ptr(), B, q_heads, q_ld, cache._ref, page_table.data_ptr(), max_pages,
+            table_ld, _vector(seq_lens, torch.int32, B, dev, "seq_lens"), D ** -0.5 if scale is None else scale, window,
+            y_ptr, _dtype_code(y), None if lse is None else lse.data_ptr(), ws.data_ptr(),
+            ws.numel() * ws.element_size())
+    return y if lse is None else (y, lse)
 
 
 def nvfp4_linear_w4a4_ws_layout(M: int, K: int) -> dict:

@@ -3,12 +3,14 @@
 // include/nvfp4.h.  Every entry point validates on the host and returns an
 // error before launching anything.
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdlib.h>
 
 #include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
+#include "kv_layout.cuh"
 
 namespace nvfp4 {
 __device__ int g_device_status = 0;
@@ -128,6 +130,7 @@ const char* nvfp4_status_string(int status) {
         case NVFP4_ERR_LAYOUT: return "scale layout not accepted by this mode";
         case NVFP4_ERR_MODE: return "unknown mode or epilogue";
         case NVFP4_ERR_DEVICE_TIMEOUT: return "a kernel's bounded wait ran out";
+        case NVFP4_ERR_PAGE: return "a cache slot, page or length on the device is out of range";
         default: return "unknown status";
     }
 }
@@ -658,6 +661,184 @@ int moe_grouped_linear(const void* x, int x_dtype, int64_t K, int gather, const 
     a.y_dtype = y_dtype;
     a.ldy = epilogue == NVFP4_EPI_SWIGLU ? N / 2 : N;
     return launch_gemv_w4a16(a, st);
+}
+
+// ---- rotary positions and the paged key-value cache ----------------------------------
+
+int nvfp4_rope_freqs(int32_t rot_dim, double theta, int scaling, double factor, double original_len, double beta_fast,
+                     double beta_slow, double* freqs, double* mscale_out) {
+    if (!freqs || !mscale_out) return NVFP4_ERR_NULL;
+    if (scaling < NVFP4_ROPE_SCALE_NONE || scaling > NVFP4_ROPE_SCALE_YARN) return NVFP4_ERR_MODE;
+    if (rot_dim < 2 || rot_dim > 1024 || rot_dim % 2 || !(theta > 0.0)) return NVFP4_ERR_SHAPE;
+    if (scaling != NVFP4_ROPE_SCALE_NONE && !(factor >= 1.0)) return NVFP4_ERR_SHAPE;
+    if (scaling == NVFP4_ROPE_SCALE_NTK && rot_dim < 4) return NVFP4_ERR_SHAPE;
+    if (scaling == NVFP4_ROPE_SCALE_YARN && (!(original_len >= 1.0) || !(beta_fast > beta_slow)))
+        return NVFP4_ERR_SHAPE;
+    if (scaling == NVFP4_ROPE_SCALE_NTK) theta *= pow(factor, (double)rot_dim / (rot_dim - 2));
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double f = pow(theta, -2.0 * i / rot_dim) / 6.283185307179586476925;
+        if (scaling == NVFP4_ROPE_SCALE_LINEAR) f /= factor;
+        if (scaling == NVFP4_ROPE_SCALE_YARN) {
+            double w = (f * original_len - beta_slow) / (beta_fast - beta_slow);
+            w = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
+            f = f * w + f / factor * (1.0 - w);
+        }
+        freqs[i] = f;
+    }
+    *mscale_out = scaling == NVFP4_ROPE_SCALE_YARN ? 0.1 * log(factor) + 1.0 : 1.0;
+    return NVFP4_OK;
+}
+
+static bool aligned8(const void* p) { return ((uintptr_t)p & 7u) == 0; }
+static bool ld_aligned(int64_t ld, int dtype) { return ld % (dtype == NVFP4_DTYPE_F32 ? 4 : 8) == 0; }
+// T rows of `cols` elements at stride ld.
+static bool rows_ok(int64_t T, int64_t cols, int64_t ld) {
+    return T >= 1 && T <= 0x7fffffff && ld >= cols && ld <= ((int64_t)1 << 40) / T;
+}
+static int rope_params_check(int32_t head_dim, int32_t rot_dim, int layout) {
+    if (layout != NVFP4_ROPE_HALF && layout != NVFP4_ROPE_INTERLEAVED) return NVFP4_ERR_LAYOUT;
+    if (rot_dim < 16 || rot_dim % 16 || rot_dim > head_dim) return NVFP4_ERR_SHAPE;
+    return NVFP4_OK;
+}
+
+int nvfp4_rope(const void* x, int x_dtype, int64_t T, int32_t heads, int32_t head_dim, int64_t x_ld,
+               const int64_t* positions, const double* freqs, int32_t rot_dim, int layout, float mscale, int inverse,
+               void* y, int y_dtype, int64_t y_ld, void* stream) {
+    if (!x || !positions || !freqs || !y) return NVFP4_ERR_NULL;
+    if (!dtype_ok(x_dtype) || !dtype_ok(y_dtype)) return NVFP4_ERR_DTYPE;
+    if (heads < 1 || heads > 65535 || head_dim < 16 || head_dim % 16 || head_dim > 1024) return NVFP4_ERR_SHAPE;
+    NVFP4_TRY(rope_params_check(head_dim, rot_dim, layout));
+    if (!rows_ok(T, (int64_t)heads * head_dim, x_ld) || !rows_ok(T, (int64_t)heads * head_dim, y_ld))
+        return NVFP4_ERR_SHAPE;
+    if (x == y && (x_dtype != y_dtype || x_ld != y_ld)) return NVFP4_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(y) || !aligned8(positions) || !aligned8(freqs) || !ld_aligned(x_ld, x_dtype) ||
+        !ld_aligned(y_ld, y_dtype))
+        return NVFP4_ERR_ALIGN;
+    NVFP4_TRY(check_arch());
+    return launch_rope(x, x_dtype, T, heads, head_dim, x_ld, positions, freqs, rot_dim, layout, mscale, inverse, y,
+                       y_dtype, y_ld, (cudaStream_t)stream);
+}
+
+static bool kv_shape_ok(int64_t num_pages, int32_t page_size, int32_t heads, int32_t head_dim, int format) {
+    if (num_pages < 1 || num_pages > 0x7fffffff || page_size < 16 || page_size % 16 || page_size > 4096 || heads < 1 ||
+        heads > 65535 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
+        return false;
+    // the bytes of a cache stay below 2^62
+    return format >= NVFP4_KV_BF16 && format <= NVFP4_KV_NVFP4 &&
+           num_pages <= ((int64_t)1 << 62) / ((int64_t)heads * (page_size / 16) * kv_tile_bytes(format, head_dim));
+}
+
+size_t nvfp4_kv_cache_bytes(int64_t num_pages, int32_t page_size, int32_t heads, int32_t head_dim, int format) {
+    if (!kv_shape_ok(num_pages, page_size, heads, head_dim, format)) return 0;
+    return (size_t)num_pages * heads * (page_size / 16) * kv_tile_bytes(format, head_dim);
+}
+
+static int kv_view(const nvfp4_kv_cache* c, KvView& v) {
+    if (!c || !c->data) return NVFP4_ERR_NULL;
+    if (c->format < NVFP4_KV_BF16 || c->format > NVFP4_KV_NVFP4) return NVFP4_ERR_MODE;
+    if (c->format != NVFP4_KV_BF16 && (!c->k_gs || !c->v_gs)) return NVFP4_ERR_NULL;
+    if (!kv_shape_ok(c->num_pages, c->page_size, c->heads, c->head_dim, c->format)) return NVFP4_ERR_SHAPE;
+    if (!aligned16(c->data) || (c->format != NVFP4_KV_BF16 &&
+                                (!elem_aligned(c->k_gs, NVFP4_DTYPE_F32) || !elem_aligned(c->v_gs, NVFP4_DTYPE_F32))))
+        return NVFP4_ERR_ALIGN;
+    v = KvView{(uint8_t*)c->data, c->k_gs, c->v_gs, c->num_pages, c->page_size, c->heads, c->head_dim, c->format};
+    return NVFP4_OK;
+}
+
+int nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k, const void* v, int x_dtype, int64_t T, int64_t k_ld,
+                   int64_t v_ld, const int64_t* slots, void* stream) {
+    KvView c;
+    NVFP4_TRY(kv_view(cache, c));
+    if (!k || !v || !slots) return NVFP4_ERR_NULL;
+    if (!dtype_ok(x_dtype)) return NVFP4_ERR_DTYPE;
+    const int64_t cols = (int64_t)c.heads * c.head_dim;
+    if (!rows_ok(T, cols, k_ld) || !rows_ok(T, cols, v_ld)) return NVFP4_ERR_SHAPE;
+    if (!aligned16(k) || !aligned16(v) || !aligned8(slots) || !ld_aligned(k_ld, x_dtype) || !ld_aligned(v_ld, x_dtype))
+        return NVFP4_ERR_ALIGN;
+    NVFP4_TRY(check_arch());
+    return launch_kv_write(c, k, v, x_dtype, T, k_ld, v_ld, slots, device_status_ptr(), (cudaStream_t)stream);
+}
+
+int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t T, void* k_out, void* v_out, int y_dtype,
+                  void* stream) {
+    KvView c;
+    NVFP4_TRY(kv_view(cache, c));
+    if (!slots || !k_out || !v_out) return NVFP4_ERR_NULL;
+    if (!dtype_ok(y_dtype)) return NVFP4_ERR_DTYPE;
+    if (!rows_ok(T, (int64_t)c.heads * c.head_dim, (int64_t)c.heads * c.head_dim)) return NVFP4_ERR_SHAPE;
+    if (!aligned16(k_out) || !aligned16(v_out) || !aligned8(slots)) return NVFP4_ERR_ALIGN;
+    NVFP4_TRY(check_arch());
+    return launch_kv_read(c, slots, T, k_out, v_out, y_dtype, device_status_ptr(), (cudaStream_t)stream);
+}
+
+int nvfp4_rope_kv_write(const nvfp4_kv_cache* cache, const void* q, const void* k, const void* v, int x_dtype,
+                        int64_t T, int32_t q_heads, int64_t q_ld, int64_t k_ld, int64_t v_ld,
+                        const int64_t* positions, const int64_t* slots, const double* freqs, int32_t rot_dim,
+                        int layout, float mscale, void* q_out, void* stream) {
+    KvView c;
+    NVFP4_TRY(kv_view(cache, c));
+    if (!q || !k || !v || !positions || !slots || !freqs || !q_out) return NVFP4_ERR_NULL;
+    if (!dtype_ok(x_dtype)) return NVFP4_ERR_DTYPE;
+    if (q_heads < 1 || q_heads > 65535) return NVFP4_ERR_SHAPE;
+    NVFP4_TRY(rope_params_check(c.head_dim, rot_dim, layout));
+    const int64_t cols = (int64_t)c.heads * c.head_dim;
+    if (!rows_ok(T, (int64_t)q_heads * c.head_dim, q_ld) || !rows_ok(T, cols, k_ld) || !rows_ok(T, cols, v_ld))
+        return NVFP4_ERR_SHAPE;
+    if (q_out == q || q_out == k || q_out == v) return NVFP4_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned8(positions) ||
+        !aligned8(slots) || !aligned8(freqs) || !ld_aligned(q_ld, x_dtype) || !ld_aligned(k_ld, x_dtype) ||
+        !ld_aligned(v_ld, x_dtype))
+        return NVFP4_ERR_ALIGN;
+    NVFP4_TRY(check_arch());
+    return launch_rope_kv_write(c, q, k, v, x_dtype, T, q_heads, q_ld, k_ld, v_ld, positions, slots, freqs, rot_dim,
+                                layout, mscale, q_out, device_status_ptr(), (cudaStream_t)stream);
+}
+
+// ---- attention of one token per sequence ---------------------------------------------
+
+size_t nvfp4_attn_decode_workspace(const nvfp4_kv_cache* cache, int64_t B, int32_t q_heads, int64_t max_pages) {
+    if (!cache || !kv_shape_ok(cache->num_pages, cache->page_size, cache->heads, cache->head_dim, cache->format))
+        return 0;
+    const KvView c{nullptr, nullptr, nullptr, cache->num_pages, cache->page_size, cache->heads, cache->head_dim,
+                   cache->format};
+    return attn_decode_workspace(c, B, q_heads, max_pages);
+}
+
+int nvfp4_attn_decode(const void* q, int64_t B, int32_t q_heads, int64_t q_ld, const nvfp4_kv_cache* cache,
+                      const int32_t* page_table, int64_t max_pages, int64_t table_ld, const int32_t* seq_lens,
+                      float scale, int32_t window, void* y, int y_dtype, float* lse, void* ws, size_t ws_bytes,
+                      void* stream) {
+    KvView c;
+    NVFP4_TRY(kv_view(cache, c));
+    if (!q || !page_table || !seq_lens || !y) return NVFP4_ERR_NULL;
+    if (!dtype_ok(y_dtype)) return NVFP4_ERR_DTYPE;
+    const size_t need = attn_decode_workspace(c, B, q_heads, max_pages);
+    if (!need || table_ld < max_pages || table_ld > ((int64_t)1 << 40) / B || window < 0 || !isfinite(scale) ||
+        !rows_ok(B, (int64_t)q_heads * c.head_dim, q_ld))
+        return NVFP4_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(y) || q_ld % 8 || ((uintptr_t)page_table & 3u) || ((uintptr_t)seq_lens & 3u) ||
+        ((uintptr_t)lse & 3u))
+        return NVFP4_ERR_ALIGN;
+    if (!ws || ws_bytes < need) return NVFP4_ERR_WORKSPACE;
+    if (!aligned16(ws)) return NVFP4_ERR_ALIGN;
+    NVFP4_TRY(check_arch());
+    AttnDecodeLaunch L{};
+    L.q = q;
+    L.B = B;
+    L.q_ld = q_ld;
+    L.q_heads = q_heads;
+    L.page_table = page_table;
+    L.max_pages = max_pages;
+    L.table_ld = table_ld;
+    L.seq_lens = seq_lens;
+    L.scale = scale;
+    L.window = window;
+    L.y = y;
+    L.y_dtype = y_dtype;
+    L.lse = lse;
+    L.ws = ws;
+    L.status = device_status_ptr();
+    return launch_attn_decode(c, L, (cudaStream_t)stream);
 }
 
 }  // extern "C"

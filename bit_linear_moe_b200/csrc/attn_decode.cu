@@ -1,0 +1,72 @@
+// Host side of the decode attention: workspace, grid and dispatch by format
+// (the kernels are in attn_decode.cuh).
+#include "attn_decode.cuh"
+
+namespace nvfp4 {
+namespace attn {
+
+int run_bf16(const Args& a, int64_t grid, int y_dtype, cudaStream_t st);
+int run_e4m3(const Args& a, int64_t grid, int y_dtype, cudaStream_t st);
+int run_nvfp4(const Args& a, int64_t grid, int y_dtype, cudaStream_t st);
+
+struct Plan {
+    int G, cols, chunks;
+    int64_t grid;
+    size_t header, bytes;
+};
+
+// The grid: two CTAs per SM, fewer when even the longest sequences leave no
+// tile for each warp.  False for shapes out of range.
+static bool plan(const KvView& c, int64_t B, int q_heads, int64_t max_pages, Plan& p) {
+    if (B < 1 || B > 4096 || q_heads < 1 || q_heads % c.heads || max_pages < 1 || max_pages > 0x7fffffff) return false;
+    p.G = q_heads / c.heads;
+    p.cols = cols_of(p.G, c.head_dim);
+    p.chunks = (p.G + p.cols - 1) / p.cols;
+    const int64_t per_seq = (int64_t)c.heads * ((p.G + 7) / 8) * (c.page_size / kKvTile);
+    if (max_pages > (int64_t)0x7fffffff / per_seq / B || max_pages > (int64_t)0x7fffffff / c.page_size) return false;
+    const int64_t tiles = B * max_pages * c.heads * p.chunks * (c.page_size / kKvTile);
+    const int64_t most = kv_tile_bytes(c.format, c.head_dim) >= 16384 ? kMaxGrid / kCtasPerSm : kMaxGrid;
+    p.grid = (tiles + 3) / 4 < most ? (tiles + 3) / 4 : most;
+    p.header = ((size_t)(B + 2) * 4 + 255) / 256 * 256;
+    p.bytes = p.header + (size_t)p.grid * 2 * p.cols * (c.head_dim + 2) * 4;
+    return true;
+}
+
+}  // namespace attn
+
+size_t attn_decode_workspace(const KvView& c, int64_t B, int q_heads, int64_t max_pages) {
+    attn::Plan p;
+    return attn::plan(c, B, q_heads, max_pages, p) ? p.bytes : 0;
+}
+
+int launch_attn_decode(const KvView& c, const AttnDecodeLaunch& L, cudaStream_t st) {
+    attn::Plan p;
+    if (!attn::plan(c, L.B, L.q_heads, L.max_pages, p)) return NVFP4_ERR_SHAPE;
+    attn::Args a{};
+    a.c = c;
+    a.q = (const __nv_bfloat16*)L.q;
+    a.q_ld = L.q_ld;
+    a.B = (int)L.B;
+    a.q_heads = L.q_heads;
+    a.G = p.G;
+    a.chunks = p.chunks;
+    a.table = L.page_table;
+    a.table_ld = L.table_ld;
+    a.max_pages = (int)L.max_pages;
+    a.lens = L.seq_lens;
+    a.scale_log2 = L.scale * 1.44269504088896340736f;
+    a.window = L.window;
+    a.y = L.y;
+    a.lse = L.lse;
+    a.header = (uint32_t*)L.ws;
+    a.partial = (float*)((char*)L.ws + p.header);
+    a.status = L.status;
+    a.zero = 0;
+    switch (c.format) {
+        case NVFP4_KV_BF16: return attn::run_bf16(a, p.grid, L.y_dtype, st);
+        case NVFP4_KV_E4M3: return attn::run_e4m3(a, p.grid, L.y_dtype, st);
+        default: return attn::run_nvfp4(a, p.grid, L.y_dtype, st);
+    }
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,897 @@
+// K11: attention of one new token per sequence over the paged key-value cache
+// (the step the dense decode stack leaves out; Ignis README, "The decode
+// round": a decode step reads what it needs once, at the card's bandwidth).
+//
+//   s_j = scale * q . k_j   over  max(0, len - window) <= j < len
+//   y   = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),   lse = ln sum_j e^(s_j)
+//
+// Bound: HBM.  Each seen cache row is read once for all query heads of its
+// key head.  At G query heads per key head a cached byte (NVFP4, D = 128)
+// carries 4 * G / 1.125 flop, so the tensor cores are far from busy; what
+// has to be watched is the number of instructions per tile.  That is why the
+// products use warp-level mma (m16n8k16): the fragments come straight from the
+// 4-bit codes in registers (no round trip of dequantized tiles through shared
+// or tensor memory), and N = 8 is the width that one token's query heads have.
+// Both products are taken transposed:
+//   S^T = K Q^T    A = 16 tokens x D (codes converted in registers), B = Q^T
+//   O^T = V^T P^T  A = D x 16 tokens, B = P^T, from S^T's accumulators by
+//                  movmatrix; token pairs of V are formed by byte permutes
+// The inner dimension of the first product may be permuted at will, so a
+// thread takes 16 contiguous bytes of a key row for its fragments; the rows
+// of the second are the head's columns, so a thread takes contiguous bytes of
+// value rows.
+//
+// Work split.  All tiles of all (sequence, key head, block of query columns)
+// segments form one list; every CTA takes an equal contiguous range of it and
+// every warp an equal range of that, whatever the lengths in the batch.  A
+// warp streams its tiles through a ring of its own (one bulk copy per tile,
+// S in flight) with its running maximum, sum and O^T in registers, and never
+// meets another warp until the end.  Segments that lie inside a warp are
+// written at once; the rest are joined per CTA through shared memory, and
+// segments that span CTAs by attn_join_kernel from the workspace, in list
+// order (the same inputs give the same bits).
+#pragma once
+
+#include <atomic>
+#include <type_traits>
+
+#include "internal.h"
+#include "kv_layout.cuh"
+#include "tma.cuh"
+
+namespace nvfp4 {
+namespace attn {
+
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxGrid = 148 * kCtasPerSm;
+
+struct Args {
+    KvView c;
+    const __nv_bfloat16* q;  // [B] rows of q_heads * D at stride q_ld
+    int64_t q_ld;
+    int B, q_heads, G, chunks;  // chunks: blocks of `cols` query heads per key head
+    const int32_t* table;       // [B, max_pages] at stride table_ld
+    int64_t table_ld;
+    int max_pages;
+    const int32_t* lens;
+    float scale_log2;  // scale * log2(e)
+    int window;        // 0: all
+    void* y;           // [B, q_heads, D]
+    float* lse;        // [B, q_heads] or null
+    uint32_t* header;  // workspace: [0] tiles per CTA, [1 .. B + 1] first tile of each sequence
+    float* partial;    // workspace: [grid][2] pieces
+    int* status;
+    uint32_t zero;     // always 0 (see refill)
+};
+
+// A piece: O [cols][D], then m [cols] (log2 units), then l [cols].
+template <int D, int NT>
+struct Piece {
+    static constexpr int kCols = 8 * NT;
+    static constexpr int kFloats = kCols * (D + 2);
+};
+
+template <int FMT, int D, int NT>
+struct Cfg {
+    static constexpr int kDb = kv_code_bytes(FMT, D), kSb = kv_scale_bytes(FMT, D);
+    static constexpr int kTile = kv_tile_bytes(FMT, D);
+    static constexpr int kPieces = kDb / 16;
+    static constexpr int kWarps = (D == 256 || kTile >= 8192 || (D == 128 && NT == 2)) ? 4 : 8;
+    // ring: about 72 KB per CTA, so that two CTAs fit an SM and some 140 KB
+    // are on their way per SM (44 bytes per ns times ~1 us of loaded latency
+    // asks for at least 44 KB)
+    static constexpr int kRing = kTile >= 16384 ? 2 : (72 * 1024) / (kWarps * kTile) > 8 ? 8 : (72 * 1024) / (kWarps * kTile);
+    static constexpr int kRingBytes = kWarps * kRing * kTile;
+    static constexpr int kPieceBytes = Piece<D, NT>::kFloats * 4;
+    static constexpr int kFixed = kRingBytes + kWarps * kPieceBytes;  // then the prefix
+    static constexpr int kMt = D / 16;                                 // 16-row tiles of O^T
+    static_assert(kRing >= 2, "one tile in flight while one is used");
+    static_assert(kRing * kTile >= kPieceBytes, "a warp's last piece goes into its ring");
+};
+
+NVFP4_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+NVFP4_DEV uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+NVFP4_DEV uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+NVFP4_DEV uint32_t pack_f16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+NVFP4_DEV uint32_t pack_b16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+NVFP4_DEV uint32_t movmatrix_trans(uint32_t a) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+template <bool BF16>
+NVFP4_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// N bytes (4, 8 or 16) of shared memory as words.
+template <int N>
+NVFP4_DEV void lds(const uint8_t* p, uint32_t (&w)[N / 4]) {
+    if constexpr (N == 16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (N == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+}
+
+// Where a tile of the list lies.
+struct Place {
+    uint32_t b, s, j, tiles;  // sequence, segment of it (key head, chunk), tile of the seen ones, their number
+};
+
+NVFP4_DEV Place place_of(uint32_t t, uint32_t hc, const uint32_t* first, uint32_t B) {
+    const uint32_t u = t / hc;
+    uint32_t lo = 0, hi = B;  // first[lo] <= u < first[hi]
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (first[mid] <= u) lo = mid;
+        else hi = mid;
+    }
+    Place p;
+    p.b = lo;
+    p.tiles = first[lo + 1] - first[lo];
+    const uint32_t rem = t - first[lo] * hc;
+    p.s = rem / p.tiles;
+    p.j = rem - p.s * p.tiles;
+    return p;
+}
+
+// Seen tokens of a sequence: [lo, len).
+NVFP4_DEV void seen_range(const Args& a, int b, int& lo, int& len) {
+    const int cap = a.max_pages * a.c.page_size;
+    len = min(max(a.lens[b], 0), cap);
+    lo = (a.window > 0 && len > a.window) ? len - a.window : 0;
+}
+
+// Writes out[v] (eight consecutive columns) of one query head.
+NVFP4_DEV void store_y8(__nv_bfloat16* p, const float (&v)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_b16(v[0], v[1]), pack_b16(v[2], v[3]), pack_b16(v[4], v[5]), pack_b16(v[6], v[7]));
+}
+NVFP4_DEV void store_y8(float* p, const float (&v)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// 1 / l, or 0 where nothing was seen (or every score is -inf).  A NaN stays.
+NVFP4_DEV float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+NVFP4_DEV float lse_of(float m, float l) {
+    return l == 0.0f ? __int_as_float(0xff800000) : (m + log2f(l)) * 0.693147180559945309f;
+}
+
+// The weights of two pieces' running maxima.
+NVFP4_DEV float weight(float m, float M) { return m == __int_as_float(0xff800000) ? 0.0f : ex2(m - M); }
+
+// One tile's work for a warp.  YT only decides whether P keeps its low part:
+// with bf16 output P is rounded to fp16 once (2^-12 of each weight, random
+// in sign, against the 2^-9 of the output's own rounding); with fp32 output,
+// and for the bf16 cache (where P has to be bf16, 2^-9), P is split into a
+// high and a low part and multiplied twice.
+template <int FMT, int D, int NT, typename YT>
+struct Warp {
+    using C = Cfg<FMT, D, NT>;
+    static constexpr bool kBf16 = FMT == NVFP4_KV_BF16;
+    static constexpr bool kSplit = kBf16 || std::is_same<YT, float>::value;
+    static constexpr int kUk = C::kDb / 4 < 16 ? C::kDb / 4 : 16;  // bytes of a key row a thread takes at a time
+    static constexpr int kNk = C::kDb / (4 * kUk);
+    static constexpr int kUv = C::kDb / 8 < 16 ? C::kDb / 8 : 16;  // bytes of a value row
+    static constexpr int kNv = C::kDb / (8 * kUv);
+    static constexpr int kPerByteX2 = FMT == NVFP4_KV_BF16 ? 1 : FMT == NVFP4_KV_E4M3 ? 2 : 4;  // elements per 2 bytes
+    static constexpr int kEk = kUk * kPerByteX2 / 2, kEv = kUv * kPerByteX2 / 2;                // elements per unit
+    static constexpr int kQw = D / 8;  // query words of a thread per column block
+
+    uint32_t q[NT][kQw];
+    float o[NT][C::kMt][4];
+    float m[NT][2], l[NT][2], f[NT][2];  // columns 2t, 2t + 1: maximum, sum (this thread's tokens), factor of the scores
+
+    // Queries of segment (b, hk, chunk): column n = lane / 4 of each block.
+    // Quantized caches multiply in fp16: the column is prescaled by a power of
+    // two that brings its largest element to [2^14, 2^15), exact for every
+    // element within 2^31 of it; the factor undoes it.
+    NVFP4_DEV void load_q(const Args& a, int b, int hk, int chunk, float gs) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int col = (chunk * NT + n) * 8 + g;
+            const bool live = col < a.G;
+            const __nv_bfloat16* qp = a.q + (int64_t)b * a.q_ld + (int64_t)(hk * a.G + col) * D;
+#pragma unroll
+            for (int i = 0; i < kNk; ++i)
+#pragma unroll
+                for (int e = 0; e < kEk / 8; ++e) {
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (live) w = *reinterpret_cast<const uint4*>(qp + kEk * (t + 4 * i) + 8 * e);
+                    const int at = i * (kEk / 2) + 4 * e;
+                    q[n][at] = w.x, q[n][at + 1] = w.y, q[n][at + 2] = w.z, q[n][at + 3] = w.w;
+                }
+            float back = 1.0f;
+            if constexpr (!kBf16) {
+                float amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kQw; ++i)
+                    amax = fmaxf(amax, fmaxf(fabsf(bf16lo_to_f32(q[n][i])), fabsf(bf16hi_to_f32(q[n][i]))));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                int p = amax > 0.0f ? 14 - ((int)(__float_as_uint(amax) >> 23) - 127) : 0;
+                p = min(max(p, -112), 112);
+                const float up = __uint_as_float((uint32_t)(127 + p) << 23);
+                back = __uint_as_float((uint32_t)(127 - p) << 23);
+#pragma unroll
+                for (int i = 0; i < kQw; ++i)
+                    q[n][i] = pack_f16(bf16lo_to_f32(q[n][i]) * up, bf16hi_to_f32(q[n][i]) * up);
+            }
+            // the factors of this thread's two score columns
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float bk = __shfl_sync(0xffffffffu, back, (2 * t + c) * 4);
+                f[n][c] = a.scale_log2 * gs * bk;
+                m[n][c] = __int_as_float(0xff800000);
+                l[n][c] = 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < C::kMt; ++k)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[n][k][c] = 0.0f;
+        }
+    }
+
+    // Block scale pair -> two fp16 duplicated words.
+    static NVFP4_DEV void scale_words(uint32_t bytes, uint32_t& s0, uint32_t& s1) {
+        const uint32_t h = e4m3x2_to_f16x2((uint16_t)bytes);
+        s0 = prmt(h, h, 0x1010);
+        s1 = prmt(h, h, 0x3232);
+    }
+
+    // Tile with tokens tok0 .. tok0 + 15; those outside [lo, len) are masked
+    // (EDGE; their bytes may be anything, NaN included).
+    template <bool EDGE>
+    NVFP4_DEV void tile(const uint8_t* tp, int tok0, int lo, int len) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const uint8_t* ks = tp + 32 * C::kDb;  // key scales, then value scales
+        // ---- S^T = K Q^T: this thread's rows g and g + 8
+        float s[NT][2][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[n][p][c] = 0.0f;
+        const int turn = kv_turn(g, C::kPieces);
+#pragma unroll
+        for (int i = 0; i < kNk; ++i) {
+            const int off = kUk * (t + 4 * i);
+            const int at = (((off >> 4) ^ turn) << 4) | (off & 15);
+            uint32_t w0[kUk / 4], w1[kUk / 4];
+            lds<kUk>(tp + g * C::kDb + at, w0);
+            lds<kUk>(tp + (g + 8) * C::kDb + at, w1);
+            if constexpr (FMT == NVFP4_KV_NVFP4) {
+                uint32_t sc[2][2];  // [row][block of the unit]
+                const uint8_t* sp = ks + g * C::kSb + (off >> 3);
+                if constexpr (kUk == 16) {
+                    scale_words(*reinterpret_cast<const uint16_t*>(sp), sc[0][0], sc[0][1]);
+                    scale_words(*reinterpret_cast<const uint16_t*>(sp + 8 * C::kSb), sc[1][0], sc[1][1]);
+                } else {
+                    uint32_t unused;
+                    scale_words(*sp, sc[0][0], unused);
+                    scale_words(sp[8 * C::kSb], sc[1][0], unused);
+                }
+#pragma unroll
+                for (int w = 0; w < kUk / 4; ++w) {
+                    uint32_t a0[4], a1[4];
+                    e2m1x8_to_f16x2(w0[w], a0);
+                    e2m1x8_to_f16x2(w1[w], a1);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {  // E2M1 x E4M3: exact in fp16
+                        a0[e] = mul_f16x2(a0[e], sc[0][w >> 1]);
+                        a1[e] = mul_f16x2(a1[e], sc[1][w >> 1]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const int at_q = i * (kEk / 2) + 4 * w + 2 * h;
+                            mma16816<false>(s[n][h], a0[2 * h], a1[2 * h], a0[2 * h + 1], a1[2 * h + 1], q[n][at_q],
+                                            q[n][at_q + 1]);
+                        }
+                }
+            } else if constexpr (FMT == NVFP4_KV_E4M3) {
+#pragma unroll
+                for (int w = 0; w < kUk / 4; ++w) {
+                    const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)w0[w]), a2 = e4m3x2_to_f16x2((uint16_t)(w0[w] >> 16));
+                    const uint32_t a1 = e4m3x2_to_f16x2((uint16_t)w1[w]), a3 = e4m3x2_to_f16x2((uint16_t)(w1[w] >> 16));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const int at_q = i * (kEk / 2) + 2 * w;
+                        mma16816<false>(s[n][w & 1], a0, a1, a2, a3, q[n][at_q], q[n][at_q + 1]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int w = 0; w < kUk / 8; ++w)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const int at_q = i * (kEk / 2) + 2 * w;
+                        mma16816<true>(s[n][w & 1], w0[2 * w], w1[2 * w], w0[2 * w + 1], w1[2 * w + 1], q[n][at_q],
+                                       q[n][at_q + 1]);
+                    }
+            }
+        }
+        // ---- softmax: tokens tok0 + g (c 0, 1) and tok0 + g + 8 (c 2, 3), columns 2t, 2t + 1
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float x[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                x[c] = (s[n][0][c] + s[n][1][c]) * f[n][c & 1];
+                if constexpr (EDGE) {
+                    const int tok = tok0 + g + 8 * (c >> 1);
+                    if (tok < lo || tok >= len) x[c] = __int_as_float(0xff800000);
+                }
+            }
+            // the running maximum is raised only when a score passes it by
+            // more than 2^8 in weight: it only guards the range (weights stay
+            // below 2^8, sums in fp32), so most tiles need no exchange
+            const float up0 = fmaxf(x[0], x[2]), up1 = fmaxf(x[1], x[3]);
+            if (__any_sync(0xffffffffu, up0 > m[n][0] + 8.0f || up1 > m[n][1] + 8.0f)) {
+                float mx[2] = {up0, up1};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], d));
+                    mx[c] = fmaxf(mx[c], m[n][c]);
+                    const float al = weight(m[n][c], mx[c]);
+                    m[n][c] = mx[c];
+                    l[n][c] *= al;
+#pragma unroll
+                    for (int k = 0; k < C::kMt; ++k) {
+                        o[n][k][c] *= al;
+                        o[n][k][2 + c] *= al;
+                    }
+                }
+            }
+            float p[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float mm = m[n][c & 1];
+                p[c] = ex2(x[c] - (mm == __int_as_float(0xff800000) ? 0.0f : mm));
+            }
+            l[n][0] += p[0] + p[2];
+            l[n][1] += p[1] + p[3];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float a = p[2 * h], b = p[2 * h + 1];
+                const uint32_t hi = kBf16 ? pack_b16(a, b) : pack_f16(a, b);
+                ph[n][h] = movmatrix_trans(hi);
+                if constexpr (kSplit) {
+                    float ra, rb;
+                    if constexpr (kBf16) {
+                        ra = a - bf16lo_to_f32(hi);
+                        rb = b - bf16hi_to_f32(hi);
+                    } else {
+                        const float2 r = f16x2_to_f32x2(hi);
+                        ra = a - r.x;
+                        rb = b - r.y;
+                    }
+                    pl[n][h] = movmatrix_trans(kBf16 ? pack_b16(ra, rb) : pack_f16(ra, rb));
+                }
+            }
+        }
+        // ---- O^T += V^T P^T: this thread's columns of tokens 2t, 2t + 1, 2t + 8, 2t + 9
+        const uint8_t* vp = tp + 16 * C::kDb;
+        const uint8_t* vs = ks + 16 * C::kSb;
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            const int off = kUv * (g + 8 * i);
+            uint32_t w[4][kUv / 4];
+            uint32_t sc[4][2];  // NVFP4: fp16 duplicated scale of each token's block(s)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = 2 * t + (k & 1) + 8 * (k >> 1);
+                lds<kUv>(vp + r * C::kDb + kv_place(r, off, C::kPieces), w[k]);
+                if constexpr (FMT == NVFP4_KV_NVFP4) {
+                    const uint8_t* sp = vs + r * C::kSb + (off >> 3);
+                    if constexpr (kUv == 16) {
+                        scale_words(*reinterpret_cast<const uint16_t*>(sp), sc[k][0], sc[k][1]);
+                    } else {
+                        uint32_t unused;
+                        scale_words(*sp, sc[k][0], unused);
+                    }
+                }
+                if constexpr (EDGE) {
+                    const int tok = tok0 + r;
+                    if (tok < lo || tok >= len) {
+#pragma unroll
+                        for (int e = 0; e < kUv / 4; ++e) w[k][e] = 0u;
+                        sc[k][0] = sc[k][1] = 0u;
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kUv / 4; ++e) {
+                constexpr int kPairs = FMT == NVFP4_KV_NVFP4 ? 4 : FMT == NVFP4_KV_E4M3 ? 2 : 1;  // per word
+                uint32_t v[4][kPairs];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (FMT == NVFP4_KV_NVFP4) {
+                        e2m1x8_to_f16x2(w[k][e], v[k]);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) v[k][x] = mul_f16x2(v[k][x], sc[k][e >> 1]);
+                    } else if constexpr (FMT == NVFP4_KV_E4M3) {
+                        v[k][0] = e4m3x2_to_f16x2((uint16_t)w[k][e]);
+                        v[k][1] = e4m3x2_to_f16x2((uint16_t)(w[k][e] >> 16));
+                    } else {
+                        v[k][0] = w[k][e];
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < kPairs; ++x) {
+                    const int mt = (i * (kUv / 4) + e) * kPairs + x;
+                    const uint32_t a0 = prmt(v[0][x], v[1][x], 0x5410), a1 = prmt(v[0][x], v[1][x], 0x7632);
+                    const uint32_t a2 = prmt(v[2][x], v[3][x], 0x5410), a3 = prmt(v[2][x], v[3][x], 0x7632);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma16816<kBf16>(o[n][mt], a0, a1, a2, a3, ph[n][0], ph[n][1]);
+                        if constexpr (kSplit) mma16816<kBf16>(o[n][mt], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+                    }
+                }
+            }
+        }
+    }
+
+    // First column (element of the head) of this thread's O^T rows of mt: rows
+    // g and g + 8 of the tile are the head's elements d and d + 1.
+    static NVFP4_DEV int column(int mt) {
+        constexpr int per_unit = kEv / 2;
+        const int g = (threadIdx.x & 31) >> 2;
+        return kEv * (g + 8 * (mt / per_unit)) + 2 * (mt % per_unit);
+    }
+
+    NVFP4_DEV void finish_sums() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], d);
+    }
+
+    // This warp's piece to `dst`.
+    NVFP4_DEV void store_piece(float* dst) {
+        const int lane = threadIdx.x & 31, t = lane & 3;
+        constexpr int cols = 8 * NT;
+        finish_sums();
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int col = n * 8 + 2 * t + c;
+#pragma unroll
+                for (int mt = 0; mt < C::kMt; ++mt)
+                    *reinterpret_cast<float2*>(dst + col * D + column(mt)) =
+                        make_float2(o[n][mt][c], o[n][mt][2 + c]);
+                if (lane < 4) {
+                    dst[cols * D + col] = m[n][c];
+                    dst[cols * D + cols + col] = l[n][c];
+                }
+            }
+    }
+
+    // A whole segment, straight to the output.
+    NVFP4_DEV void store_output(const Args& a, int b, int hk, int chunk) {
+        const int lane = threadIdx.x & 31, t = lane & 3;
+        finish_sums();
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int col = (chunk * NT + n) * 8 + 2 * t + c;
+                if (col >= a.G) continue;
+                const int64_t row = (int64_t)b * a.q_heads + hk * a.G + col;
+                const float inv = inverse_sum(l[n][c]);
+                YT* yp = (YT*)a.y + row * D;
+#pragma unroll
+                for (int mt = 0; mt < C::kMt; mt += 4) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[2 * e] = o[n][mt + e][c] * inv;
+                        v[2 * e + 1] = o[n][mt + e][2 + c] * inv;
+                    }
+                    store_y8(yp + column(mt), v);
+                }
+                if (a.lse && lane < 4) a.lse[row] = lse_of(m[n][c], l[n][c]);
+            }
+    }
+};
+
+template <int FMT, int D, int NT, typename YT>
+__global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>::kTile >= 16384 ? 1 : kCtasPerSm)
+    attn_decode_kernel(const Args a) {
+    using C = Cfg<FMT, D, NT>;
+    constexpr int W = C::kWarps, S = C::kRing, kCols = 8 * NT;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* ring_all = smem;
+    float* pieces = reinterpret_cast<float*>(smem + C::kRingBytes);
+    uint32_t* first = reinterpret_cast<uint32_t*>(smem + C::kFixed);  // [B + 1]
+    __shared__ uint64_t s_full[W][S];
+    __shared__ uint32_t s_seg[2 * W], s_scan[W], s_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    griddep_launch_dependents();
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(&s_full[warp][i], 1);
+        fence_barrier_init();
+    }
+    if (lane < 2) s_seg[2 * warp + lane] = 0xffffffffu;
+    griddep_wait();
+
+    // ---- the list: first tile of each sequence (in tiles of one segment)
+    const uint32_t B = (uint32_t)a.B;
+    uint32_t carry = 0;
+    for (uint32_t b0 = 0; b0 < B; b0 += W * 32) {
+        const uint32_t b = b0 + threadIdx.x;
+        uint32_t n = 0;
+        if (b < B) {
+            int lo, len;
+            seen_range(a, (int)b, lo, len);
+            if (a.lens[b] > len && a.lens[b] > 0 && a.status) atomicExch(a.status, NVFP4_ERR_PAGE);
+            n = len > lo ? (uint32_t)((len + kKvTile - 1) / kKvTile - lo / kKvTile) : 0u;
+        }
+        uint32_t x = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) s_scan[warp] = x;
+        __syncthreads();
+        uint32_t before = carry, all = 0;
+        for (int w = 0; w < W; ++w) {
+            const uint32_t v = s_scan[w];
+            if (w < warp) before += v;
+            all += v;
+        }
+        if (b < B) first[b] = before + x - n;
+        carry += all;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) first[B] = carry;
+    __syncthreads();
+
+    const uint32_t hc = (uint32_t)(a.c.heads * a.chunks);
+    const uint32_t total = carry * hc;
+    uint32_t per_cta = (total + gridDim.x - 1) / gridDim.x;
+    if (per_cta < (uint32_t)W) per_cta = W;
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) a.header[0] = per_cta;
+        for (uint32_t b = threadIdx.x; b <= B; b += W * 32) a.header[1 + b] = first[b];
+    }
+    const uint32_t t0 = min(total, per_cta * blockIdx.x), t1 = min(total, t0 + per_cta);
+    const uint32_t n_cta = t1 - t0;
+    const uint32_t w0 = t0 + (n_cta / W) * warp + min(n_cta % W, (uint32_t)warp);
+    const uint32_t n_warp = n_cta / W + ((uint32_t)warp < n_cta % W ? 1u : 0u);
+
+    // ---- this warp's tiles
+    uint8_t* ring = ring_all + (size_t)warp * S * C::kTile;
+    uint64_t* full = s_full[warp];
+    float* my_first = pieces + warp * Piece<D, NT>::kFloats;
+    float* my_last = reinterpret_cast<float*>(ring);
+    const uint32_t tiles_per_page = (uint32_t)(a.c.page_size / kKvTile);
+    if (n_warp > 0) {
+        // addresses of tiles 32 k .. 32 k + 31, one per lane
+        const uint8_t* addr = nullptr;
+        auto look_up = [&](uint32_t i0) {
+            const uint32_t i = i0 + lane;
+            if (i < n_warp) {
+                const Place p = place_of(w0 + i, hc, first, B);
+                int lo, len;
+                seen_range(a, (int)p.b, lo, len);
+                const uint32_t jt = (uint32_t)(lo / kKvTile) + p.j;
+                const uint32_t pi = jt / tiles_per_page;
+                int64_t page = a.table[(int64_t)p.b * a.table_ld + pi];
+                if (page < 0 || page >= a.c.num_pages) {  // reported; page 0 is read in its place
+                    if (a.status) atomicExch(a.status, NVFP4_ERR_PAGE);
+                    page = 0;
+                }
+                const uint32_t hk = p.s / (uint32_t)a.chunks;
+                addr = a.c.data + ((page * a.c.heads + hk) * tiles_per_page + (jt - pi * tiles_per_page)) * C::kTile;
+            }
+        };
+        // `dep` is made of registers that hold the results of everything read
+        // from the slot; adding dep & 0 to the byte count makes the copy wait
+        // for those reads to have returned (a.zero is 0 at run time).
+        auto refill = [&](uint32_t i, uint32_t dep) {
+            if (i < n_warp && lane == (int)(i & 31)) {
+                const uint32_t slot = i % S;
+                const uint32_t bytes = (uint32_t)C::kTile + (dep & a.zero);
+                mbar_expect_tx(&full[slot], bytes);
+                bulk_load(ring + slot * C::kTile, addr, bytes, &full[slot]);
+            }
+        };
+        look_up(0);
+        for (uint32_t i = 0; i < (uint32_t)S; ++i) refill(i, 0u);
+
+        Warp<FMT, D, NT, YT> wk;
+        float k_gs = 1.0f;
+        float v_gs = 1.0f;
+        if constexpr (FMT != NVFP4_KV_BF16) {
+            k_gs = *a.c.k_gs;
+            v_gs = *a.c.v_gs;
+        }
+        Place at = place_of(w0, hc, first, B);
+        int lo = 0, len = 0;
+        uint32_t begun = at.j;  // tile of the segment this piece starts with
+        bool fresh = true;
+        for (uint32_t i = 0; i < n_warp; ++i) {
+            const uint32_t hk = at.s / (uint32_t)a.chunks, chunk = at.s - hk * (uint32_t)a.chunks;
+            if (fresh) {
+                seen_range(a, (int)at.b, lo, len);
+                wk.load_q(a, (int)at.b, (int)hk, (int)chunk, k_gs);
+                begun = at.j;
+                fresh = false;
+            }
+            const uint32_t slot = i % S;
+            const bool ok = mbar_wait(&full[slot], (i / S) & 1, a.status);
+            if (!__all_sync(0xffffffffu, ok)) {
+                // a copy that never arrived: wait (again bounded) for the others and stop
+                for (uint32_t k = i + 1; k < i + S && k < n_warp; ++k) mbar_wait(&full[k % S], (k / S) & 1, a.status);
+                break;
+            }
+            const uint8_t* tp = ring + slot * C::kTile;
+            const int tok0 = (lo / kKvTile + (int)at.j) * kKvTile;
+            if (tok0 >= lo && tok0 + kKvTile <= len) wk.template tile<false>(tp, tok0, lo, len);
+            else wk.template tile<true>(tp, tok0, lo, len);
+            uint32_t dep = 0;
+#pragma unroll
+            for (int k = 0; k < C::kMt; ++k) dep ^= __float_as_uint(wk.o[0][k][0]);
+            const uint32_t next = i + S;
+            if ((next & 31) == 0) look_up(next);
+            refill(next, dep);
+            // ---- end of the segment or of the range
+            const bool ends = at.j + 1 == at.tiles;
+            if (ends || i + 1 == n_warp) {
+                // the values' global scale
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < C::kMt; ++k)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if constexpr (FMT != NVFP4_KV_BF16) wk.o[n][k][c] *= v_gs;
+                if (ends && begun == 0) {
+                    wk.store_output(a, (int)at.b, (int)hk, (int)chunk);
+                } else {
+                    const uint32_t id = first[at.b] * hc + at.s * at.tiles;  // the segment's first tile names it
+                    wk.store_piece(ends ? my_first : my_last);
+                    if (lane == 0) s_seg[2 * warp + (ends ? 0 : 1)] = id;
+                }
+                fresh = true;
+            }
+            if (!ends) {
+                ++at.j;
+            } else {
+                at.j = 0;
+                if (++at.s == hc) {
+                    at.s = 0;
+                    do ++at.b;
+                    while (at.b < B && first[at.b + 1] == first[at.b]);
+                    if (at.b < B) at.tiles = first[at.b + 1] - first[at.b];
+                }
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- segments that several warps share, in list order
+    for (int p0 = 0; p0 < 2 * W;) {
+        const uint32_t id = s_seg[p0];
+        if (id == 0xffffffffu) {
+            ++p0;
+            continue;
+        }
+        int p1 = p0 + 1;  // pieces p0 .. p1 - 1 of segment `id` (absent ones in between)
+        for (int p = p1; p < 2 * W; ++p) {
+            if (s_seg[p] == id) p1 = p + 1;
+            else if (s_seg[p] != 0xffffffffu) break;
+        }
+        const Place at = place_of(id, hc, first, B);
+        const uint32_t hk = at.s / (uint32_t)a.chunks, chunk = at.s - hk * (uint32_t)a.chunks;
+        const bool whole = id >= t0 && id + at.tiles <= t1;
+        float* part = a.partial + ((int64_t)blockIdx.x * 2 + (id >= t0 ? 1 : 0)) * Piece<D, NT>::kFloats;
+        auto piece = [&](int p) -> const float* {
+            return (p & 1) ? reinterpret_cast<const float*>(ring_all + (size_t)(p >> 1) * S * C::kTile)
+                           : pieces + (p >> 1) * Piece<D, NT>::kFloats;
+        };
+        for (int e = threadIdx.x; e < kCols * (D / 8); e += W * 32) {
+            const int col = e / (D / 8), d = (e % (D / 8)) * 8;
+            float M = __int_as_float(0xff800000);
+            for (int p = p0; p < p1; ++p)
+                if (s_seg[p] == id) M = fmaxf(M, piece(p)[kCols * D + col]);
+            float v[8], L = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+            for (int p = p0; p < p1; ++p) {
+                if (s_seg[p] != id) continue;
+                const float* src = piece(p);
+                const float w = weight(src[kCols * D + col], M);
+                L += w * src[kCols * D + kCols + col];
+                const float4 x = *reinterpret_cast<const float4*>(src + col * D + d);
+                const float4 y = *reinterpret_cast<const float4*>(src + col * D + d + 4);
+                v[0] += w * x.x, v[1] += w * x.y, v[2] += w * x.z, v[3] += w * x.w;
+                v[4] += w * y.x, v[5] += w * y.y, v[6] += w * y.z, v[7] += w * y.w;
+            }
+            if (whole) {
+                const int qc = (int)chunk * kCols + col;
+                if (qc < a.G) {
+                    const int64_t row = (int64_t)at.b * a.q_heads + hk * a.G + qc;
+                    const float inv = inverse_sum(L);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] *= inv;
+                    store_y8((YT*)a.y + row * D + d, v);
+                    if (a.lse && d == 0) a.lse[row] = lse_of(M, L);
+                }
+            } else {
+                store_y8(part + col * D + d, v);
+                if (d == 0) {
+                    part[kCols * D + col] = M;
+                    part[kCols * D + kCols + col] = L;
+                }
+            }
+        }
+        p0 = p1;
+    }
+}
+
+// Joins the segments that several CTAs share and writes zeros for sequences
+// without tokens: one block of lanes per output row, pieces in list order.
+// kRows rows per CTA: 8 (a warp each) or 1 (eight warps, each every eighth
+// piece; for few rows of many pieces).
+template <int D, int NT, typename YT, int kRows>
+__global__ void __launch_bounds__(256) attn_join_kernel(const Args a) {
+    constexpr int kCols = 8 * NT, kV = D / 32;  // floats per lane
+    griddep_launch_dependents();
+    griddep_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = kRows == 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kRows + warp;
+    if (row >= (int64_t)a.B * a.q_heads) return;
+    const int b = (int)(row / a.q_heads), hq = (int)(row - (int64_t)b * a.q_heads);
+    const int hk = hq / a.G, gq = hq - hk * a.G, chunk = gq / kCols, col = gq - chunk * kCols;
+    const uint32_t per = a.header[0], f0 = a.header[1 + b], f1 = a.header[2 + b];
+    const uint32_t tiles = f1 - f0, hc = (uint32_t)(a.c.heads * a.chunks);
+    YT* yp = (YT*)a.y + row * D;
+    if (tiles == 0) {
+        if (kRows == 1 && warp) return;
+        for (int k = 0; k < kV; ++k) store_out<YT>(yp + lane + 32 * k, 0.0f);
+        if (a.lse && lane == 0) a.lse[row] = __int_as_float(0xff800000);
+        return;
+    }
+    const uint32_t ts = f0 * hc + (uint32_t)(hk * a.chunks + chunk) * tiles;
+    const uint32_t c0 = ts / per, c1 = (ts + tiles - 1) / per;
+    if (c0 == c1) return;
+    const int step = kRows == 1 ? 8 : 1, off = kRows == 1 ? warp : 0;
+    auto part = [&](uint32_t c) { return a.partial + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * Piece<D, NT>::kFloats; };
+    // maximum over the pieces, lanes striding over them
+    float M = __int_as_float(0xff800000);
+    for (uint32_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c)[kCols * D + col]);
+    M = warp_max(M);
+    float v[kV], L = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) v[k] = 0.0f;
+#pragma unroll 4
+    for (uint32_t c = c0 + off; c <= c1; c += step) {
+        const float* src = part(c);
+        const float w = weight(src[kCols * D + col], M);
+        L += w * src[kCols * D + kCols + col];
+#pragma unroll
+        for (int k = 0; k < kV; ++k) v[k] += w * src[col * D + lane + 32 * k];
+    }
+    if constexpr (kRows == 1) {
+        __shared__ float s_v[8][D + 1];
+#pragma unroll
+        for (int k = 0; k < kV; ++k) s_v[warp][lane + 32 * k] = v[k];
+        if (lane == 0) s_v[warp][D] = L;
+        __syncthreads();
+        if (warp) return;
+        L = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) v[k] = 0.0f;
+        for (int w = 0; w < 8; ++w) {
+            L += s_v[w][D];
+#pragma unroll
+            for (int k = 0; k < kV; ++k) v[k] += s_v[w][lane + 32 * k];
+        }
+    }
+    const float inv = inverse_sum(L);
+#pragma unroll
+    for (int k = 0; k < kV; ++k) store_out<YT>(yp + lane + 32 * k, v[k] * inv);
+    if (a.lse && lane == 0) a.lse[row] = lse_of(M, L);
+}
+
+template <int FMT, int D, int NT, typename YT>
+static int run(const Args& a, int64_t grid, cudaStream_t st) {
+    using C = Cfg<FMT, D, NT>;
+    struct Once {  // one flag per instantiation and device
+        static int set(int bytes) {
+            static std::atomic<uint64_t> done{0};
+            int dev = 0;
+            if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return NVFP4_ERR_LAUNCH;
+            if (done.load(std::memory_order_relaxed) >> dev & 1) return NVFP4_OK;
+            if (cudaFuncSetAttribute(attn_decode_kernel<FMT, D, NT, YT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     bytes) != cudaSuccess)
+                return NVFP4_ERR_LAUNCH;
+            done.fetch_or(1ull << dev, std::memory_order_relaxed);
+            return NVFP4_OK;
+        }
+    };
+    constexpr int kMostB = 4096;
+    NVFP4_TRY_INTERNAL(Once::set(C::kFixed + (kMostB + 4) * 4));
+    cudaLaunchAttribute attr[1];
+    set_pdl_attr(attr[0]);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(C::kWarps * 32);
+    cfg.dynamicSmemBytes = (size_t)C::kFixed + (size_t)((a.B + 4) / 4 * 4) * 4 + 16;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, attn_decode_kernel<FMT, D, NT, YT>, a) != cudaSuccess) return NVFP4_ERR_LAUNCH;
+    // the join: a warp per row, or a CTA per row where rows may have many pieces
+    const int64_t rows = (int64_t)a.B * a.q_heads;
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    cudaError_t e;
+    if ((int64_t)a.B * a.c.heads * a.chunks * 8 > grid) {
+        cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+        e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D, NT, YT, 8>, a);
+    } else {
+        cfg.gridDim = dim3((unsigned)rows);
+        e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D, NT, YT, 1>, a);
+    }
+    return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+}
+
+// Query columns per pass: 16 where the key head has more than 8 query heads
+// and O^T fits the registers (D <= 128), else 8.
+constexpr int cols_of(int G, int D) { return (G > 8 && D <= 128) ? 16 : 8; }
+
+template <int FMT, typename YT>
+static int run_fmt(const Args& a, int64_t grid, cudaStream_t st) {
+    const bool two = cols_of(a.G, a.c.head_dim) == 16;
+    switch (a.c.head_dim) {
+        case 64: return two ? run<FMT, 64, 2, YT>(a, grid, st) : run<FMT, 64, 1, YT>(a, grid, st);
+        case 128: return two ? run<FMT, 128, 2, YT>(a, grid, st) : run<FMT, 128, 1, YT>(a, grid, st);
+        case 256: return run<FMT, 256, 1, YT>(a, grid, st);
+        default: return NVFP4_ERR_SHAPE;
+    }
+}
+
+}  // namespace attn
+}  // namespace nvfp4

@@ -1,0 +1,13 @@
+// Instantiations of the decode attention kernels for the nvfp4 cache
+// (attn_decode.cuh), one file per format so that they compile in parallel.
+#include "attn_decode.cuh"
+
+namespace nvfp4 {
+namespace attn {
+
+int run_nvfp4(const Args& a, int64_t grid, int y_dtype, cudaStream_t st) {
+    return y_dtype == NVFP4_DTYPE_BF16 ? run_fmt<NVFP4_KV_NVFP4, __nv_bfloat16>(a, grid, st) : run_fmt<NVFP4_KV_NVFP4, float>(a, grid, st);
+}
+
+}  // namespace attn
+}  // namespace nvfp4

@@ -179,6 +179,40 @@ int launch_calibrate(const float* w, int64_t N, int64_t K, const void* x, int64_
                      uint8_t* scales, float* gs_out, float* col_scale_out, float* err_out, int32_t* alpha_idx_out,
                      const CalibrateWs& ws, cudaStream_t st);
 
+// kv_cache.cu: rotary positions and the paged key-value cache.
+struct KvView;  // kv_layout.cuh
+int launch_rope(const void* x, int x_dtype, int64_t T, int heads, int D, int64_t x_ld, const int64_t* positions,
+                const double* freqs, int rot, int layout, float mscale, int inverse, void* y, int y_dtype,
+                int64_t y_ld, cudaStream_t st);
+int launch_kv_write(const KvView& c, const void* k, const void* v, int x_dtype, int64_t T, int64_t k_ld, int64_t v_ld,
+                    const int64_t* slots, int* status, cudaStream_t st);
+int launch_kv_read(const KvView& c, const int64_t* slots, int64_t T, void* k_out, void* v_out, int y_dtype,
+                   int* status, cudaStream_t st);
+int launch_rope_kv_write(const KvView& c, const void* q, const void* k, const void* v, int x_dtype, int64_t T,
+                         int q_heads, int64_t q_ld, int64_t k_ld, int64_t v_ld, const int64_t* positions,
+                         const int64_t* slots, const double* freqs, int rot, int layout, float mscale, void* q_out,
+                         int* status, cudaStream_t st);
+
+// attn_decode.cu: attention of one token per sequence over the paged cache.
+struct AttnDecodeLaunch {
+    const void* q;
+    int64_t B, q_ld;
+    int q_heads;
+    const int32_t* page_table;
+    int64_t max_pages, table_ld;
+    const int32_t* seq_lens;
+    float scale;
+    int window;
+    void* y;
+    int y_dtype;
+    float* lse;
+    void* ws;
+    int* status;
+};
+// Bytes of workspace; 0 for shapes out of range.
+size_t attn_decode_workspace(const KvView& c, int64_t B, int q_heads, int64_t max_pages);
+int launch_attn_decode(const KvView& c, const AttnDecodeLaunch& L, cudaStream_t st);
+
 #define NVFP4_TRY_INTERNAL(expr)        \
     do {                                \
         const int _s = (expr);          \

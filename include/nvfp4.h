@@ -69,8 +69,10 @@ enum {
     NVFP4_ERR_LAUNCH = 7,         /* a kernel launch or driver call failed        */
     NVFP4_ERR_LAYOUT = 8,         /* scale layout not accepted by the chosen mode */
     NVFP4_ERR_MODE = 9,           /* unknown mode or epilogue code                */
-    NVFP4_ERR_DEVICE_TIMEOUT = 10 /* a kernel's bounded wait ran out (read with
+    NVFP4_ERR_DEVICE_TIMEOUT = 10, /* a kernel's bounded wait ran out (read with
                                      nvfp4_read_device_status)                    */
+    NVFP4_ERR_PAGE = 11           /* a cache slot, page or length on the device is
+                                     out of range (nvfp4_read_device_status)      */
 };
 
 /* ---- enumerations ------------------------------------------------------ */
@@ -94,6 +96,12 @@ enum { NVFP4_MODE_AUTO = 0, NVFP4_MODE_W4A16 = 1, NVFP4_MODE_W4A4 = 2 };
 
 /* Epilogues of moe_grouped_linear. */
 enum { NVFP4_EPI_NONE = 0, NVFP4_EPI_SWIGLU = 1, NVFP4_EPI_COMBINE = 2 };
+
+/* Formats of the key-value cache, layouts of rotary pairs, and ways to stretch
+ * rotary frequencies over long contexts. */
+enum { NVFP4_KV_BF16 = 0, NVFP4_KV_E4M3 = 1, NVFP4_KV_NVFP4 = 2 };
+enum { NVFP4_ROPE_HALF = 0, NVFP4_ROPE_INTERLEAVED = 1 };
+enum { NVFP4_ROPE_SCALE_NONE = 0, NVFP4_ROPE_SCALE_LINEAR = 1, NVFP4_ROPE_SCALE_NTK = 2, NVFP4_ROPE_SCALE_YARN = 3 };
 
 /* ---- helpers ------------------------------------------------------------ */
 
@@ -444,6 +452,151 @@ int moe_grouped_linear(const void* x, int x_dtype, int64_t K, int gather,
  * Requires K % 256 == 0 and the other limits of moe_grouped_linear. */
 int moe_grouped_linear_w4a4_ws_layout(int64_t R, int64_t K, int64_t N, int32_t E, int32_t k, int epilogue,
                                       int64_t out[6]);
+
+/* ---- rotary positions -------------------------------------------------------
+ * The steps between the QKV linear and the output linear of a decode stack
+ * (Ignis README, "The decode round": a decode step streams the whole stack
+ * once; the pages leave positions, cache and attention open).
+ *
+ * nvfp4_rope_freqs (host only, no device work): fills freqs[rot_dim / 2] (HOST
+ * memory) with each pair's frequency in TURNS per token (radians / 2 pi),
+ *     f_i = theta^(-2i / rot_dim) / (2 pi)
+ * stretched for contexts `factor` times longer than the model was trained on:
+ *     NONE    f_i                                    (factor ignored)
+ *     LINEAR  f_i / factor
+ *     NTK     theta replaced by theta * factor^(rot_dim / (rot_dim - 2))
+ *     YARN    f_i (w + (1 - w) / factor), w = clamp((f_i * original_len -
+ *             beta_slow) / (beta_fast - beta_slow), 0, 1): pairs that turn
+ *             beta_fast times or more within original_len keep their
+ *             frequency, those that turn beta_slow times or less are
+ *             interpolated; cos and sin get the magnitude 0.1 ln(factor) + 1
+ * and *mscale_out with the magnitude (1 but for YARN).  Copy freqs to the
+ * device for the calls below.  Requires rot_dim % 2 == 0, 2 <= rot_dim <=
+ * 1024 (NTK: rot_dim >= 4), theta > 0, and, where they are used, factor >= 1,
+ * original_len >= 1, beta_fast > beta_slow; ERR_SHAPE otherwise. */
+int nvfp4_rope_freqs(int32_t rot_dim, double theta, int scaling, double factor, double original_len,
+                     double beta_fast, double beta_slow, double* freqs, double* mscale_out);
+
+/* nvfp4_rope:  rotary positions.  With a = 2 pi frac(positions[t] * freqs[i])
+ * (the product and its fraction in binary64), c = fp32(mscale * cos a) and
+ * s = fp32(mscale * sin a), pair i of each head turns by
+ *     (u, v) -> (u c - v s, v c + u s)        (fp32, each product and sum rounded)
+ *   HALF         u = x[i],  v = x[i + rot_dim / 2]
+ *   INTERLEAVED  u = x[2i], v = x[2i + 1]
+ * and elements rot_dim .. head_dim - 1 pass through; y is rounded to y_dtype.
+ * inverse != 0 turns back (-a; also the gradient's rotation).
+ *   x          [T] rows at stride x_ld elements, each `heads` heads of
+ *              head_dim (a column slice of the QKV output is read in place)
+ *   positions  [T] int64, of magnitude below 2^53 (negative ones turn back)
+ *   freqs      [rot_dim / 2] binary64, turns per token (nvfp4_rope_freqs)
+ *   y          rows at stride y_ld.  y == x (same dtype and stride) rotates
+ *              in place; otherwise x and y must not overlap.
+ * Requires head_dim % 16 == 0, head_dim <= 1024, rot_dim % 16 == 0, 16 <=
+ * rot_dim <= head_dim, T >= 1, x and y 16-byte aligned with strides of a
+ * multiple of 8 (BF16) or 4 (F32) elements; positions and freqs 8-byte. */
+int nvfp4_rope(const void* x, int x_dtype, int64_t T, int32_t heads, int32_t head_dim, int64_t x_ld,
+               const int64_t* positions, const double* freqs, int32_t rot_dim, int layout, float mscale, int inverse,
+               void* y, int y_dtype, int64_t y_ld, void* stream);
+
+/* ---- paged key-value cache ----------------------------------------------------
+ * The keys and values of every sequence, in pages of page_size tokens:
+ *   BF16   the values
+ *   E4M3   E4M3 codes; value = E4M3(code) * gs       code = E4M3(x / gs), saturating
+ *   NVFP4  value = E2M1(code) * E4M3(scale) * gs, the codes and block scales
+ *          nvfp4_quantize gives each 16 elements with gs_in = gs
+ * with one fp32 gs for the keys and one for the values (device; not read for
+ * BF16).  `data` is [num_pages][heads][page_size / 16] tiles of 16 tokens, each
+ * tile the 16 key rows, the 16 value rows (head_dim codes each, packed as
+ * elsewhere), then for NVFP4 16 + 16 rows of head_dim / 16 scale bytes.  The
+ * 16-byte pieces of the codes of a tile's row r (n of them) are permuted:
+ * piece c is stored at c ^ (((r & 6) ^ ((r & 1) << 2)) & (n - 1)).  A page is
+ * one contiguous run of bytes.  Token o of page p is SLOT p * page_size + o.
+ * Requires page_size a multiple of 16 up to 4096, head_dim 64, 128 or 256,
+ * heads 1 .. 65535, num_pages 1 .. 2^31 - 1, data 16-byte aligned. */
+typedef struct {
+    void* data;          /* nvfp4_kv_cache_bytes(...) bytes */
+    const float* k_gs;   /* one device float (NULL for BF16) */
+    const float* v_gs;
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t heads;       /* key (= value) heads */
+    int32_t head_dim;
+    int32_t format;      /* NVFP4_KV_* */
+} nvfp4_kv_cache;
+
+/* Bytes of a cache's data (0 on bad arguments). */
+size_t nvfp4_kv_cache_bytes(int64_t num_pages, int32_t page_size, int32_t heads, int32_t head_dim, int format);
+
+/* nvfp4_kv_write:  token t's keys and values to slot slots[t].
+ *   cache  HOST pointer to the description (copied by the call)
+ *   k, v   [T] rows at strides k_ld, v_ld elements, each cache->heads heads of
+ *          head_dim, x_dtype F32 or BF16
+ *   slots  [T] int64.  A negative slot is skipped (padding); slots at or past
+ *          num_pages * page_size are skipped and reported as NVFP4_ERR_PAGE
+ *          in the device status word.  Slots >= 0 must be distinct.
+ * Nothing but the named tokens' rows is written.  E4M3 and NVFP4 take finite
+ * values.  Requires T >= 1, 16-byte aligned k and v with strides of a multiple
+ * of 8 (BF16) or 4 (F32) elements. */
+int nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k, const void* v, int x_dtype, int64_t T, int64_t k_ld,
+                   int64_t v_ld, const int64_t* slots, void* stream);
+
+/* nvfp4_kv_read:  the rows of slots[t], dequantized (fp32 product, rounded to
+ * y_dtype), dense.
+ *   k_out, v_out  [T, heads, head_dim] in y_dtype (F32 or BF16)
+ * A negative slot gives zeros; one out of range gives zeros and is reported as
+ * NVFP4_ERR_PAGE.  A slot may be read more than once. */
+int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t T, void* k_out, void* v_out, int y_dtype,
+                  void* stream);
+
+/* nvfp4_rope_kv_write:  nvfp4_rope of the queries and keys and nvfp4_kv_write
+ * of the rotated keys and the values, in one pass over the QKV rows.  Bit for
+ * bit what the separate calls give with the rotated keys in BF16:
+ *     q_out = nvfp4_rope(q) (BF16);   cache <- nvfp4_kv_write(nvfp4_rope(k) (BF16), v)
+ *   q      [T] rows of q_heads heads at stride q_ld;  k, v as nvfp4_kv_write
+ *   q_out  [T, q_heads, head_dim] bf16 (rows of padding tokens are rotated too)
+ * Requires what the two calls require; q_out must not overlap q, k or v. */
+int nvfp4_rope_kv_write(const nvfp4_kv_cache* cache, const void* q, const void* k, const void* v, int x_dtype,
+                        int64_t T, int32_t q_heads, int64_t q_ld, int64_t k_ld, int64_t v_ld,
+                        const int64_t* positions, const int64_t* slots, const double* freqs, int32_t rot_dim,
+                        int layout, float mscale, void* q_out, void* stream);
+
+/* ---- nvfp4_attn_decode ----------------------------------------------------------
+ * Attention of one new token per sequence over the paged cache.  For sequence
+ * b, query head h, key head h / (q_heads / heads):
+ *     s_j = scale * q[b, h] . k_j     for max(0, len - window) <= j < len
+ *     y[b, h] = sum_j e^(s_j) v_j / sum_j e^(s_j),   lse[b, h] = ln sum_j e^(s_j)
+ * with len = seq_lens[b] (the new token's own row, already written, included).
+ * A sequence with len <= 0 gives y = 0 and lse = -inf, and so does a row whose
+ * scores are all -inf.  Rows behind len may hold anything; a NaN or infinity
+ * in a seen value makes that element of the output not finite.
+ *   q           [B] rows of q_heads * head_dim bf16 at stride q_ld
+ *   page_table  [B] rows of max_pages int32 at stride table_ld: page of tokens
+ *               i * page_size ..; only the entries of seen tokens are read.
+ *               Sequences may share pages.
+ *   seq_lens    [B] int32
+ *   window      0: no limit; else the number of last tokens seen
+ *   y           [B, q_heads, head_dim] in y_dtype (F32 or BF16)
+ *   lse         NULL or [B, q_heads] fp32
+ *   ws          scratch of nvfp4_attn_decode_workspace(...) bytes; contents on
+ *               entry are ignored.
+ * A page index out of range, or a length above max_pages * page_size, is
+ * reported as NVFP4_ERR_PAGE in the device status word; that sequence's output
+ * is then unspecified (nothing out of range is read).
+ * Numerics: scores, softmax sums and outputs accumulate in fp32.  Quantized
+ * caches are multiplied exactly (E2M1 x E4M3 in fp16); queries enter as fp16
+ * after a per-head power-of-two prescale (exact for elements within 2^31 of
+ * the head's largest).  Softmax weights are rounded to fp16 for bf16 output and
+ * carry a second, low part for fp32 output and the BF16 cache.  The result
+ * does not depend on anything but the arguments' shapes and values: the same
+ * call gives the same bits.
+ * Requires 1 <= B <= 4096, q_heads a multiple of cache->heads, max_pages >= 1,
+ * at most 2^31 - 1 tiles of 16 tokens in all (B * max_pages * page_size / 16 *
+ * heads * ceil(q_heads / heads / 8)), q and y 16-byte aligned, q_ld % 8 == 0. */
+size_t nvfp4_attn_decode_workspace(const nvfp4_kv_cache* cache, int64_t B, int32_t q_heads, int64_t max_pages);
+int nvfp4_attn_decode(const void* q, int64_t B, int32_t q_heads, int64_t q_ld, const nvfp4_kv_cache* cache,
+                      const int32_t* page_table, int64_t max_pages, int64_t table_ld, const int32_t* seq_lens,
+                      float scale, int32_t window, void* y, int y_dtype, float* lse, void* ws, size_t ws_bytes,
+                      void* stream);
 
 #ifdef __cplusplus
 }
