@@ -90,11 +90,11 @@ def lib() -> ctypes.CDLL:
             "nvfp4_rms_norm_quant_workspace": (sz, [i64]),
             "nvfp4_rms_norm_quant": (i, [p, i, i64, i64, i64, i, p, p, p, p, sz, p]),
             "nvfp4_rope_freqs": (i, [i32, f64, i, f64, f64, f64, f64, p, p]),
-            "nvfp4_rope": (i, [p, i, i64, i32, i32, i64, p, p, i32, i, f32, i, p, i, i64, p]),
+            "nvfp4_rope": (i, [p, i, i64, i32, i32, i64, p, p, i32, i, f64, i, p, i, i64, p]),
             "nvfp4_kv_cache_bytes": (sz, [i64, i32, i32, i32, i]),
             "nvfp4_kv_write": (i, [p, p, p, i, i64, i64, i64, p, p]),
             "nvfp4_kv_read": (i, [p, p, i64, p, p, i, p]),
-            "nvfp4_rope_kv_write": (i, [p, p, p, p, i, i64, i32, i64, i64, i64, p, p, p, i32, i, f32, p, p]),
+            "nvfp4_rope_kv_write": (i, [p, p, p, p, i, i64, i32, i64, i64, i64, p, p, p, i32, i, f64, p, p]),
             "nvfp4_attn_decode_workspace": (sz, [p, i64, i32, i64]),
             "nvfp4_attn_decode": (i, [p, i64, i32, i64, p, p, i64, i64, p, f32, i32, p, i, p, p, sz, p]),
             "moe_route_topk_workspace": (sz, [i64, i32, i32]),
@@ -398,29 +398,39 @@ def moe_layer_decode(h: torch.Tensor, w_router: torch.Tensor, k: int, gate_up, d
 # ---- rotary positions, the paged key-value cache, attention of one new token -------
 
 
+# The current stream's handle by device index (the public call builds a Stream object: 3 us
+# of a decode step's enqueue time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(dev: torch.device, name: str, *args):
     """Call a C entry point on ``dev``'s current stream (made the current device for
     the call when it is not)."""
-    if dev.index != torch.cuda.current_device():
+    index = dev.index
+    if index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _launch(dev, name, *args)
-    status = getattr(_lib or lib(), name)(*args, torch.cuda.current_stream().cuda_stream)
+    status = getattr(_lib or lib(), name)(*args, _raw_stream(index))
     if status != OK:
         raise NVFP4Error(status, name)
 
 
-def _heads_view(t: torch.Tensor, what: str, shape=None) -> int:
-    """Row stride (elements) of a ``[rows, heads, head_dim]`` view whose heads are
-    packed, as a slice of fused QKV rows is."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+def _heads_view(t: torch.Tensor, dev, what: str, T=None, heads=None, head_dim=None) -> int:
+    """Row stride (elements) of a ``[rows, heads, head_dim]`` view on ``dev`` whose heads
+    are packed, as a slice of fused QKV rows is."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
         raise ValueError(f"{what} must be a [rows, heads, head_dim] view with packed heads")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    if T is not None and (shape[0] != T or shape[1] != heads or shape[2] != head_dim):
+        raise ValueError(f"{what} must have shape {(T, heads, head_dim)}, not {tuple(shape)}")
+    if t.device != dev:
+        raise ValueError(f"{what} must be on {dev}, not {t.device}")
+    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _vector(t: torch.Tensor, dtype, n: int | None, dev, what: str) -> int:
-    """Address of a contiguous vector of ``n`` elements of ``dtype`` on ``dev``."""
+    """Address of a contiguous tensor of ``n`` elements of ``dtype`` on ``dev``."""
     if t.dtype != dtype or not t.is_contiguous() or (n is not None and t.numel() != n):
         raise ValueError(f"{what} must be a contiguous {dtype} tensor" + (f" of {n} elements" if n is not None else ""))
     if t.device != dev:
@@ -428,11 +438,9 @@ def _vector(t: torch.Tensor, dtype, n: int | None, dev, what: str) -> int:
     return t.data_ptr()
 
 
-def _cuda(t: torch.Tensor, what: str, dev=None) -> torch.device:
+def _cuda(t: torch.Tensor, what: str) -> torch.device:
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{what} must be on {dev}, not {t.device}")
     return t.device
 
 
@@ -493,14 +501,13 @@ def nvfp4_rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, la
     is read in place).  ``positions [T]`` int64, ``freqs`` from :func:`nvfp4_rope_freqs`
     on x's device.  ``y=x`` rotates in place."""
     dev = _cuda(x, "x")
-    x_ld = _heads_view(x, "x")
+    x_ld = _heads_view(x, dev, "x")
     T, heads, D = x.shape
     if y is None:
-        y = torch.empty((T, heads, D), dtype=y_dtype, device=dev)
+        y = x.new_empty((T, heads, D), dtype=y_dtype)
         y_ld = heads * D
     else:
-        _cuda(y, "y", dev)
-        y_ld = _heads_view(y, "y", x.shape)
+        y_ld = _heads_view(y, dev, "y", T, heads, D)
     _launch(dev, "nvfp4_rope", x.data_ptr(), _dtype_code(x), T, heads, D, x_ld,
             _vector(positions, torch.int64, T, dev, "positions"), _vector(freqs, torch.float64, None, dev, "freqs"),
             2 * freqs.numel(), layout, mscale, int(inverse), y.data_ptr(), _dtype_code(y), y_ld)
@@ -511,13 +518,12 @@ def nvfp4_kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torc
     """Write token t's keys and values (``[T, heads, head_dim]`` views, fp32 or bf16) to
     slot ``slots[t]`` (int64; page * page_size + offset; negative: skipped)."""
     dev = cache.device
-    shape = (k.shape[0], cache.heads, cache.head_dim)
-    _cuda(k, "k", dev), _cuda(v, "v", dev)
-    k_ld, v_ld = _heads_view(k, "k", shape), _heads_view(v, "v", shape)
+    T, heads, D = k.shape[0], cache.heads, cache.head_dim
+    k_ld, v_ld = _heads_view(k, dev, "k", T, heads, D), _heads_view(v, dev, "v", T, heads, D)
     if k.dtype != v.dtype:
         raise TypeError("k and v must have one dtype")
-    _launch(dev, "nvfp4_kv_write", cache._ref, k.data_ptr(), v.data_ptr(), _dtype_code(k), shape[0], k_ld, v_ld,
-            _vector(slots, torch.int64, shape[0], dev, "slots"))
+    _launch(dev, "nvfp4_kv_write", cache._ref, k.data_ptr(), v.data_ptr(), _dtype_code(k), T, k_ld, v_ld,
+            _vector(slots, torch.int64, T, dev, "slots"))
 
 
 def nvfp4_kv_read(cache: KVCache, slots: torch.Tensor, k_out=None, v_out=None, y_dtype=torch.bfloat16):
@@ -527,9 +533,9 @@ def nvfp4_kv_read(cache: KVCache, slots: torch.Tensor, k_out=None, v_out=None, y
     T = slots.numel()
     shape = (T, cache.heads, cache.head_dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=y_dtype if v_out is None else v_out.dtype, device=dev)
+        k_out = cache.data.new_empty(shape, dtype=y_dtype if v_out is None else v_out.dtype)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=k_out.dtype, device=dev)
+        v_out = cache.data.new_empty(shape, dtype=k_out.dtype)
     if k_out.dtype != v_out.dtype:
         raise TypeError("k_out and v_out must have one dtype")
     code, n = _dtype_code(k_out), T * cache.heads * cache.head_dim
@@ -545,20 +551,18 @@ def nvfp4_rope_kv_write(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: tor
     one pass over the QKV rows; returns the rotated queries ``[T, q_heads, head_dim]``
     (bf16).  Same bits as :func:`nvfp4_rope` and :func:`nvfp4_kv_write`."""
     dev = cache.device
-    T, q_heads = q.shape[0], q.shape[1]
-    _cuda(q, "q", dev), _cuda(k, "k", dev), _cuda(v, "v", dev)
-    shape = (T, cache.heads, cache.head_dim)
-    q_ld = _heads_view(q, "q", (T, q_heads, cache.head_dim))
-    k_ld, v_ld = _heads_view(k, "k", shape), _heads_view(v, "v", shape)
+    T, q_heads, heads, D = q.shape[0], q.shape[1], cache.heads, cache.head_dim
+    q_ld = _heads_view(q, dev, "q", T, q_heads, D)
+    k_ld, v_ld = _heads_view(k, dev, "k", T, heads, D), _heads_view(v, dev, "v", T, heads, D)
     if q.dtype != k.dtype or k.dtype != v.dtype:
         raise TypeError("q, k and v must have one dtype")
     if q_out is None:
-        q_out = torch.empty((T, q_heads, cache.head_dim), dtype=torch.bfloat16, device=dev)
+        q_out = q.new_empty((T, q_heads, D), dtype=torch.bfloat16)
     _launch(dev, "nvfp4_rope_kv_write", cache._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), T,
             q_heads, q_ld, k_ld, v_ld, _vector(positions, torch.int64, T, dev, "positions"),
             _vector(slots, torch.int64, T, dev, "slots"), _vector(freqs, torch.float64, None, dev, "freqs"),
             2 * freqs.numel(), layout, mscale,
-            _vector(q_out, torch.bfloat16, T * q_heads * cache.head_dim, dev, "q_out"))
+            _vector(q_out, torch.bfloat16, T * q_heads * D, dev, "q_out"))
     return q_out
 
 
@@ -573,10 +577,8 @@ def nvfp4_attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     ``scale`` defaults to ``head_dim ** -0.5``.  Returns ``y [B, q_heads, head_dim]``,
     or ``(y, lse [B, q_heads])``."""
     dev = cache.device
-    _cuda(q, "q", dev)
-    B, q_heads = q.shape[0], q.shape[1]
-    D = cache.head_dim
-    q_ld = _heads_view(q, "q", (B, q_heads, D))
+    B, q_heads, D = q.shape[0], q.shape[1], cache.head_dim
+    q_ld = _heads_view(q, dev, "q", B, q_heads, D)
     if q.dtype != torch.bfloat16:
         raise TypeError(f"q must be bfloat16, not {q.dtype}")
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
@@ -585,13 +587,13 @@ def nvfp4_attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     max_pages = page_table.shape[1]
     table_ld = page_table.stride(0) if B > 1 else max_pages
     if y is None:
-        y = torch.empty((B, q_heads, D), dtype=y_dtype, device=dev)
+        y = q.new_empty((B, q_heads, D), dtype=y_dtype)
     y_ptr = _vector(y, y.dtype, B * q_heads * D, dev, "y")
     lse = torch.empty((B, q_heads), dtype=torch.float32, device=dev) if want_lse else None
     if ws is None:
         ws = torch.empty(nvfp4_attn_decode_workspace(cache, B, q_heads, max_pages), dtype=torch.uint8, device=dev)
-    else:
-        _cuda(ws, "ws", dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {dev}")
     _launch(dev, "nvfp4_attn_decode", q.data_ptr(), B, q_heads, q_ld, cache._ref, page_table.data_ptr(), max_pages,
             table_ld, _vector(seq_lens, torch.int32, B, dev, "seq_lens"), D ** -0.5 if scale is None else scale, window,
             y_ptr, _dtype_code(y), None if lse is None else lse.data_ptr(), ws.data_ptr(),

@@ -702,7 +702,7 @@ static int rope_params_check(int32_t head_dim, int32_t rot_dim, int layout) {
 }
 
 int nvfp4_rope(const void* x, int x_dtype, int64_t T, int32_t heads, int32_t head_dim, int64_t x_ld,
-               const int64_t* positions, const double* freqs, int32_t rot_dim, int layout, float mscale, int inverse,
+               const int64_t* positions, const double* freqs, int32_t rot_dim, int layout, double mscale, int inverse,
                void* y, int y_dtype, int64_t y_ld, void* stream) {
     if (!x || !positions || !freqs || !y) return NVFP4_ERR_NULL;
     if (!dtype_ok(x_dtype) || !dtype_ok(y_dtype)) return NVFP4_ERR_DTYPE;
@@ -774,7 +774,7 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t T, 
 int nvfp4_rope_kv_write(const nvfp4_kv_cache* cache, const void* q, const void* k, const void* v, int x_dtype,
                         int64_t T, int32_t q_heads, int64_t q_ld, int64_t k_ld, int64_t v_ld,
                         const int64_t* positions, const int64_t* slots, const double* freqs, int32_t rot_dim,
-                        int layout, float mscale, void* q_out, void* stream) {
+                        int layout, double mscale, void* q_out, void* stream) {
     KvView c;
     NVFP4_TRY(kv_view(cache, c));
     if (!q || !k || !v || !positions || !slots || !freqs || !q_out) return NVFP4_ERR_NULL;

@@ -91,7 +91,7 @@ struct Cfg {
 
 NVFP4_DEV float ex2(float x) {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 NVFP4_DEV uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
@@ -125,6 +125,25 @@ NVFP4_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, ui
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Codes to fp16 without the conversion unit (16 lanes per clock and SM, which
+// alone would hold NVFP4 at 0.7 of the memory's rate): an E2M1 code's exponent
+// and mantissa bits put at the top of fp16's mantissa and the bottom of its
+// exponent are the value times 2^-14, subnormals included; E4M3's likewise,
+// times 2^-8.
+// Eight E2M1 codes -> four pairs (i, i + 4) of value * 2^-14.
+NVFP4_DEV void e2m1x8_to_f16x2_bits(uint32_t w, uint32_t (&h)[4]) {
+    h[0] = ((w << 12) & 0x80008000u) | ((w << 9) & 0x0E000E00u);
+    h[1] = ((w << 8) & 0x80008000u) | ((w << 5) & 0x0E000E00u);
+    h[2] = ((w << 4) & 0x80008000u) | ((w << 1) & 0x0E000E00u);
+    h[3] = (w & 0x80008000u) | ((w >> 3) & 0x0E000E00u);
+}
+// Four E4M3 codes -> pairs (0, 1) and (2, 3) of value * 2^-8 (no NaN codes).
+NVFP4_DEV void e4m3x4_to_f16x2_bits(uint32_t w, uint32_t& h0, uint32_t& h1) {
+    const uint32_t a = prmt(w, 0u, 0x1404), b = prmt(w, 0u, 0x3424);
+    h0 = (a & 0x80008000u) | ((a >> 1) & 0x3F803F80u);
+    h1 = (b & 0x80008000u) | ((b >> 1) & 0x3F803F80u);
 }
 
 // N bytes (4, 8 or 16) of shared memory as words.
@@ -206,6 +225,11 @@ struct Warp {
     static constexpr int kPerByteX2 = FMT == NVFP4_KV_BF16 ? 1 : FMT == NVFP4_KV_E4M3 ? 2 : 4;  // elements per 2 bytes
     static constexpr int kEk = kUk * kPerByteX2 / 2, kEv = kUv * kPerByteX2 / 2;                // elements per unit
     static constexpr int kQw = D / 8;  // query words of a thread per column block
+    // NVFP4 key words of a unit that are converted with bit operations (the
+    // others and the values use the conversion unit): balances the two.
+    static constexpr int kBitsFrom = 1;
+    // what the key products come out divided by (bit conversions)
+    static constexpr float kUp = FMT == NVFP4_KV_NVFP4 ? 128.0f : FMT == NVFP4_KV_E4M3 ? 256.0f : 1.0f;
 
     uint32_t q[NT][kQw];
     float o[NT][C::kMt][4];
@@ -247,11 +271,20 @@ struct Warp {
                 for (int i = 0; i < kQw; ++i)
                     q[n][i] = pack_f16(bf16lo_to_f32(q[n][i]) * up, bf16hi_to_f32(q[n][i]) * up);
             }
+            if constexpr (FMT == NVFP4_KV_NVFP4) {  // words of bit-converted keys pair elements i, i + 4
+#pragma unroll
+                for (int i = 0; i < kQw; i += 4)
+                    if ((i / 4) % (kUk / 4) >= kBitsFrom) {
+                        const uint32_t a0 = q[n][i], a1 = q[n][i + 1], a2 = q[n][i + 2], a3 = q[n][i + 3];
+                        q[n][i] = prmt(a0, a2, 0x5410), q[n][i + 1] = prmt(a0, a2, 0x7632);
+                        q[n][i + 2] = prmt(a1, a3, 0x5410), q[n][i + 3] = prmt(a1, a3, 0x7632);
+                    }
+            }
             // the factors of this thread's two score columns
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const float bk = __shfl_sync(0xffffffffu, back, (2 * t + c) * 4);
-                f[n][c] = a.scale_log2 * gs * bk;
+                f[n][c] = a.scale_log2 * gs * bk * kUp;
                 m[n][c] = __int_as_float(0xff800000);
                 l[n][c] = 0.0f;
             }
@@ -262,11 +295,23 @@ struct Warp {
         }
     }
 
-    // Block scale pair -> two fp16 duplicated words.
-    static NVFP4_DEV void scale_words(uint32_t bytes, uint32_t& s0, uint32_t& s1) {
-        const uint32_t h = e4m3x2_to_f16x2((uint16_t)bytes);
-        s0 = prmt(h, h, 0x1010);
-        s1 = prmt(h, h, 0x3232);
+    // Scales of one key row's block(s) of a unit: fp16 pairs of scale * 2^-7 for
+    // the converted word(s) and scale * 2^7 for the bit-converted ones, so that
+    // both products are value * scale * 2^-7 (exact: all of E2M1 x E4M3 times
+    // 2^-7 is a multiple of 2^-17 below 2^5 with 6 significant bits).
+    struct KeyScale {
+        uint32_t lo0, hi[2];
+    };
+    static NVFP4_DEV KeyScale key_scale(const uint8_t* p) {
+        uint32_t h;
+        KeyScale k;
+        if constexpr (kUk == 16) h = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(p));
+        else h = e4m3x2_to_f16x2(*p);
+        const uint32_t up = mul_f16x2(h, 0x58005800u);  // 2^7
+        k.lo0 = mul_f16x2(prmt(h, h, 0x1010), 0x20002000u);  // 2^-7
+        k.hi[0] = prmt(up, up, 0x1010);
+        k.hi[1] = prmt(up, up, 0x3232);
+        return k;
     }
 
     // Tile with tokens tok0 .. tok0 + 15; those outside [lo, len) are masked
@@ -292,25 +337,22 @@ struct Warp {
             lds<kUk>(tp + g * C::kDb + at, w0);
             lds<kUk>(tp + (g + 8) * C::kDb + at, w1);
             if constexpr (FMT == NVFP4_KV_NVFP4) {
-                uint32_t sc[2][2];  // [row][block of the unit]
                 const uint8_t* sp = ks + g * C::kSb + (off >> 3);
-                if constexpr (kUk == 16) {
-                    scale_words(*reinterpret_cast<const uint16_t*>(sp), sc[0][0], sc[0][1]);
-                    scale_words(*reinterpret_cast<const uint16_t*>(sp + 8 * C::kSb), sc[1][0], sc[1][1]);
-                } else {
-                    uint32_t unused;
-                    scale_words(*sp, sc[0][0], unused);
-                    scale_words(sp[8 * C::kSb], sc[1][0], unused);
-                }
+                const KeyScale sc0 = key_scale(sp), sc1 = key_scale(sp + 8 * C::kSb);
 #pragma unroll
                 for (int w = 0; w < kUk / 4; ++w) {
                     uint32_t a0[4], a1[4];
-                    e2m1x8_to_f16x2(w0[w], a0);
-                    e2m1x8_to_f16x2(w1[w], a1);
+                    if (w < kBitsFrom) {
+                        e2m1x8_to_f16x2(w0[w], a0);
+                        e2m1x8_to_f16x2(w1[w], a1);
+                    } else {
+                        e2m1x8_to_f16x2_bits(w0[w], a0);
+                        e2m1x8_to_f16x2_bits(w1[w], a1);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {  // E2M1 x E4M3: exact in fp16
-                        a0[e] = mul_f16x2(a0[e], sc[0][w >> 1]);
-                        a1[e] = mul_f16x2(a1[e], sc[1][w >> 1]);
+                    for (int e = 0; e < 4; ++e) {
+                        a0[e] = mul_f16x2(a0[e], w < kBitsFrom ? sc0.lo0 : sc0.hi[w >> 1]);
+                        a1[e] = mul_f16x2(a1[e], w < kBitsFrom ? sc1.lo0 : sc1.hi[w >> 1]);
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
@@ -324,8 +366,9 @@ struct Warp {
             } else if constexpr (FMT == NVFP4_KV_E4M3) {
 #pragma unroll
                 for (int w = 0; w < kUk / 4; ++w) {
-                    const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)w0[w]), a2 = e4m3x2_to_f16x2((uint16_t)(w0[w] >> 16));
-                    const uint32_t a1 = e4m3x2_to_f16x2((uint16_t)w1[w]), a3 = e4m3x2_to_f16x2((uint16_t)(w1[w] >> 16));
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_f16x2_bits(w0[w], a0, a2);
+                    e4m3x4_to_f16x2_bits(w1[w], a1, a3);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const int at_q = i * (kEk / 2) + 2 * w;
@@ -411,59 +454,76 @@ struct Warp {
         for (int i = 0; i < kNv; ++i) {
             const int off = kUv * (g + 8 * i);
             uint32_t w[4][kUv / 4];
-            uint32_t sc[4][2];  // NVFP4: fp16 duplicated scale of each token's block(s)
+            uint32_t sb[4];  // NVFP4: block scale byte(s) of each token
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int r = 2 * t + (k & 1) + 8 * (k >> 1);
                 lds<kUv>(vp + r * C::kDb + kv_place(r, off, C::kPieces), w[k]);
                 if constexpr (FMT == NVFP4_KV_NVFP4) {
                     const uint8_t* sp = vs + r * C::kSb + (off >> 3);
-                    if constexpr (kUv == 16) {
-                        scale_words(*reinterpret_cast<const uint16_t*>(sp), sc[k][0], sc[k][1]);
-                    } else {
-                        uint32_t unused;
-                        scale_words(*sp, sc[k][0], unused);
-                    }
+                    if constexpr (kUv == 16) sb[k] = *reinterpret_cast<const uint16_t*>(sp);
+                    else sb[k] = *sp;
                 }
                 if constexpr (EDGE) {
                     const int tok = tok0 + r;
                     if (tok < lo || tok >= len) {
 #pragma unroll
                         for (int e = 0; e < kUv / 4; ++e) w[k][e] = 0u;
-                        sc[k][0] = sc[k][1] = 0u;
+                        sb[k] = 0u;
                     }
                 }
             }
+            // a word's codes of two tokens -> fp16 / bf16 pairs (token, next token)
+            // of one column each: v[2 x + p][y], column 2 y + p, tokens of pair x
+            constexpr int kPairs = FMT == NVFP4_KV_NVFP4 ? 4 : FMT == NVFP4_KV_E4M3 ? 2 : 1;  // columns / 2 per word
 #pragma unroll
             for (int e = 0; e < kUv / 4; ++e) {
-                constexpr int kPairs = FMT == NVFP4_KV_NVFP4 ? 4 : FMT == NVFP4_KV_E4M3 ? 2 : 1;  // per word
                 uint32_t v[4][kPairs];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t p = w[2 * x][e], r = w[2 * x + 1][e];
                     if constexpr (FMT == NVFP4_KV_NVFP4) {
-                        e2m1x8_to_f16x2(w[k][e], v[k]);
+                        e2m1x8_to_f16x2((p & 0x0F0F0F0Fu) | ((r << 4) & 0xF0F0F0F0u), v[2 * x]);
+                        e2m1x8_to_f16x2(((p >> 4) & 0x0F0F0F0Fu) | (r & 0xF0F0F0F0u), v[2 * x + 1]);
+                        const uint32_t sc =
+                            e4m3x2_to_f16x2((uint16_t)prmt(sb[2 * x], sb[2 * x + 1], (e >> 1) ? 0x0051 : 0x0040));
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) v[k][x] = mul_f16x2(v[k][x], sc[k][e >> 1]);
+                        for (int y = 0; y < 4; ++y) {
+                            v[2 * x][y] = mul_f16x2(v[2 * x][y], sc);
+                            v[2 * x + 1][y] = mul_f16x2(v[2 * x + 1][y], sc);
+                        }
                     } else if constexpr (FMT == NVFP4_KV_E4M3) {
-                        v[k][0] = e4m3x2_to_f16x2((uint16_t)w[k][e]);
-                        v[k][1] = e4m3x2_to_f16x2((uint16_t)(w[k][e] >> 16));
+                        const uint32_t a = prmt(p, r, 0x5140), b = prmt(p, r, 0x7362);
+                        v[2 * x][0] = e4m3x2_to_f16x2((uint16_t)a);
+                        v[2 * x + 1][0] = e4m3x2_to_f16x2((uint16_t)(a >> 16));
+                        v[2 * x][1] = e4m3x2_to_f16x2((uint16_t)b);
+                        v[2 * x + 1][1] = e4m3x2_to_f16x2((uint16_t)(b >> 16));
                     } else {
-                        v[k][0] = w[k][e];
+                        v[2 * x][0] = prmt(p, r, 0x5410);
+                        v[2 * x + 1][0] = prmt(p, r, 0x7632);
                     }
                 }
 #pragma unroll
-                for (int x = 0; x < kPairs; ++x) {
-                    const int mt = (i * (kUv / 4) + e) * kPairs + x;
-                    const uint32_t a0 = prmt(v[0][x], v[1][x], 0x5410), a1 = prmt(v[0][x], v[1][x], 0x7632);
-                    const uint32_t a2 = prmt(v[2][x], v[3][x], 0x5410), a3 = prmt(v[2][x], v[3][x], 0x7632);
+                for (int y = 0; y < kPairs; ++y) {
+                    const int mt = (i * (kUv / 4) + e) * kPairs + y;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        mma16816<kBf16>(o[n][mt], a0, a1, a2, a3, ph[n][0], ph[n][1]);
-                        if constexpr (kSplit) mma16816<kBf16>(o[n][mt], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+                        mma16816<kBf16>(o[n][mt], v[0][y], v[1][y], v[2][y], v[3][y], ph[n][0], ph[n][1]);
+                        if constexpr (kSplit)
+                            mma16816<kBf16>(o[n][mt], v[0][y], v[1][y], v[2][y], v[3][y], pl[n][0], pl[n][1]);
                     }
                 }
             }
         }
+    }
+
+    // A value that depends on everything the tile read from shared memory: one
+    // accumulator of each value unit (the scores, hence all keys, feed them all).
+    NVFP4_DEV uint32_t depend() const {
+        uint32_t d = 0;
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) d ^= __float_as_uint(o[0][i * (C::kMt / kNv)][0]);
+        return d;
     }
 
     // First column (element of the head) of this thread's O^T rows of mt: rows
@@ -628,16 +688,15 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
         // `dep` is made of registers that hold the results of everything read
         // from the slot; adding dep & 0 to the byte count makes the copy wait
         // for those reads to have returned (a.zero is 0 at run time).
-        auto refill = [&](uint32_t i, uint32_t dep) {
+        auto refill = [&](uint32_t i, uint32_t slot, uint32_t dep) {
             if (i < n_warp && lane == (int)(i & 31)) {
-                const uint32_t slot = i % S;
                 const uint32_t bytes = (uint32_t)C::kTile + (dep & a.zero);
                 mbar_expect_tx(&full[slot], bytes);
                 bulk_load(ring + slot * C::kTile, addr, bytes, &full[slot]);
             }
         };
         look_up(0);
-        for (uint32_t i = 0; i < (uint32_t)S; ++i) refill(i, 0u);
+        for (uint32_t i = 0; i < (uint32_t)S; ++i) refill(i, i, 0u);
 
         Warp<FMT, D, NT, YT> wk;
         float k_gs = 1.0f;
@@ -647,34 +706,34 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
             v_gs = *a.c.v_gs;
         }
         Place at = place_of(w0, hc, first, B);
-        int lo = 0, len = 0;
+        int lo = 0, len = 0, tok0 = 0;
         uint32_t begun = at.j;  // tile of the segment this piece starts with
+        uint32_t hk = 0, chunk = 0, slot = 0, phase = 0;
         bool fresh = true;
         for (uint32_t i = 0; i < n_warp; ++i) {
-            const uint32_t hk = at.s / (uint32_t)a.chunks, chunk = at.s - hk * (uint32_t)a.chunks;
             if (fresh) {
                 seen_range(a, (int)at.b, lo, len);
+                tok0 = (lo / kKvTile + (int)at.j) * kKvTile;
+                hk = at.s / (uint32_t)a.chunks;
+                chunk = at.s - hk * (uint32_t)a.chunks;
                 wk.load_q(a, (int)at.b, (int)hk, (int)chunk, k_gs);
                 begun = at.j;
                 fresh = false;
             }
-            const uint32_t slot = i % S;
-            const bool ok = mbar_wait(&full[slot], (i / S) & 1, a.status);
+            const bool ok = mbar_wait(&full[slot], phase, a.status);
             if (!__all_sync(0xffffffffu, ok)) {
                 // a copy that never arrived: wait (again bounded) for the others and stop
                 for (uint32_t k = i + 1; k < i + S && k < n_warp; ++k) mbar_wait(&full[k % S], (k / S) & 1, a.status);
                 break;
             }
             const uint8_t* tp = ring + slot * C::kTile;
-            const int tok0 = (lo / kKvTile + (int)at.j) * kKvTile;
             if (tok0 >= lo && tok0 + kKvTile <= len) wk.template tile<false>(tp, tok0, lo, len);
             else wk.template tile<true>(tp, tok0, lo, len);
-            uint32_t dep = 0;
-#pragma unroll
-            for (int k = 0; k < C::kMt; ++k) dep ^= __float_as_uint(wk.o[0][k][0]);
             const uint32_t next = i + S;
             if ((next & 31) == 0) look_up(next);
-            refill(next, dep);
+            refill(next, slot, wk.depend());
+            tok0 += kKvTile;
+            if (++slot == (uint32_t)S) slot = 0, phase ^= 1;
             // ---- end of the segment or of the range
             const bool ends = at.j + 1 == at.tiles;
             if (ends || i + 1 == n_warp) {

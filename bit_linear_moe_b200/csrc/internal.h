@@ -182,7 +182,7 @@ int launch_calibrate(const float* w, int64_t N, int64_t K, const void* x, int64_
 // kv_cache.cu: rotary positions and the paged key-value cache.
 struct KvView;  // kv_layout.cuh
 int launch_rope(const void* x, int x_dtype, int64_t T, int heads, int D, int64_t x_ld, const int64_t* positions,
-                const double* freqs, int rot, int layout, float mscale, int inverse, void* y, int y_dtype,
+                const double* freqs, int rot, int layout, double mscale, int inverse, void* y, int y_dtype,
                 int64_t y_ld, cudaStream_t st);
 int launch_kv_write(const KvView& c, const void* k, const void* v, int x_dtype, int64_t T, int64_t k_ld, int64_t v_ld,
                     const int64_t* slots, int* status, cudaStream_t st);
@@ -190,7 +190,7 @@ int launch_kv_read(const KvView& c, const int64_t* slots, int64_t T, void* k_out
                    int* status, cudaStream_t st);
 int launch_rope_kv_write(const KvView& c, const void* q, const void* k, const void* v, int x_dtype, int64_t T,
                          int q_heads, int64_t q_ld, int64_t k_ld, int64_t v_ld, const int64_t* positions,
-                         const int64_t* slots, const double* freqs, int rot, int layout, float mscale, void* q_out,
+                         const int64_t* slots, const double* freqs, int rot, int layout, double mscale, void* q_out,
                          int* status, cudaStream_t st);
 
 // attn_decode.cu: attention of one token per sequence over the paged cache.

@@ -62,7 +62,7 @@ struct RopeParams {
     const double* freqs;       // [pairs], turns per token
     int pairs;                 // rot_dim / 2, a multiple of 8 (0: no rotation)
     int layout;                // NVFP4_ROPE_HALF / INTERLEAVED
-    float mscale;
+    double mscale;
     int inverse;
 };
 
@@ -74,7 +74,7 @@ NVFP4_DEV void rope_angles(const RopeParams& rp, int64_t t0, int nt, float2* cs)
         double s, c;
         sincospi(2.0 * (turns - rint(turns)), &s, &c);
         if (rp.inverse) s = -s;
-        cs[i] = make_float2((float)(c * (double)rp.mscale), (float)(s * (double)rp.mscale));
+        cs[i] = make_float2((float)(c * rp.mscale), (float)(s * rp.mscale));
     }
 }
 
@@ -473,7 +473,7 @@ static cudaLaunchConfig_t pdl_config(cudaLaunchAttribute* attr, int64_t T, int h
 }
 
 int launch_rope(const void* x, int x_dtype, int64_t T, int heads, int D, int64_t x_ld, const int64_t* positions,
-                const double* freqs, int rot, int layout, float mscale, int inverse, void* y, int y_dtype,
+                const double* freqs, int rot, int layout, double mscale, int inverse, void* y, int y_dtype,
                 int64_t y_ld, cudaStream_t st) {
     const RopeParams rp{positions, freqs, rot / 2, layout, mscale, inverse};
     int tt, hc;
@@ -524,7 +524,7 @@ int launch_kv_write(const KvView& c, const void* k, const void* v, int x_dtype, 
 
 int launch_rope_kv_write(const KvView& c, const void* q, const void* k, const void* v, int x_dtype, int64_t T,
                          int q_heads, int64_t q_ld, int64_t k_ld, int64_t v_ld, const int64_t* positions,
-                         const int64_t* slots, const double* freqs, int rot, int layout, float mscale, void* q_out,
+                         const int64_t* slots, const double* freqs, int rot, int layout, double mscale, void* q_out,
                          int* status, cudaStream_t st) {
     KvWriteArgs a{};
     a.c = c;

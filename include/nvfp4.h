@@ -495,7 +495,7 @@ int nvfp4_rope_freqs(int32_t rot_dim, double theta, int scaling, double factor, 
  * rot_dim <= head_dim, T >= 1, x and y 16-byte aligned with strides of a
  * multiple of 8 (BF16) or 4 (F32) elements; positions and freqs 8-byte. */
 int nvfp4_rope(const void* x, int x_dtype, int64_t T, int32_t heads, int32_t head_dim, int64_t x_ld,
-               const int64_t* positions, const double* freqs, int32_t rot_dim, int layout, float mscale, int inverse,
+               const int64_t* positions, const double* freqs, int32_t rot_dim, int layout, double mscale, int inverse,
                void* y, int y_dtype, int64_t y_ld, void* stream);
 
 /* ---- paged key-value cache ----------------------------------------------------
@@ -558,7 +558,7 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t T, 
 int nvfp4_rope_kv_write(const nvfp4_kv_cache* cache, const void* q, const void* k, const void* v, int x_dtype,
                         int64_t T, int32_t q_heads, int64_t q_ld, int64_t k_ld, int64_t v_ld,
                         const int64_t* positions, const int64_t* slots, const double* freqs, int32_t rot_dim,
-                        int layout, float mscale, void* q_out, void* stream);
+                        int layout, double mscale, void* q_out, void* stream);
 
 /* ---- nvfp4_attn_decode ----------------------------------------------------------
  * Attention of one new token per sequence over the paged cache.  For sequence
