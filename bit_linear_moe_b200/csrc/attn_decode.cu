@@ -5,13 +5,13 @@
 namespace nvfp4 {
 namespace attn {
 
-int run_bf16(const Args& a, int64_t grid, int y_dtype, cudaStream_t st);
-int run_e4m3(const Args& a, int64_t grid, int y_dtype, cudaStream_t st);
-int run_nvfp4(const Args& a, int64_t grid, int y_dtype, cudaStream_t st);
+int run_bf16(const Args& a, const Shape& sh, int y_dtype, cudaStream_t st);
+int run_e4m3(const Args& a, const Shape& sh, int y_dtype, cudaStream_t st);
+int run_nvfp4(const Args& a, const Shape& sh, int y_dtype, cudaStream_t st);
 
 struct Plan {
     int G, cols, chunks;
-    int64_t grid;
+    Shape shape;
     size_t header, bytes;
 };
 
@@ -26,9 +26,10 @@ static bool plan(const KvView& c, int64_t B, int q_heads, int64_t max_pages, Pla
     if (max_pages > (int64_t)0x7fffffff / per_seq / B || max_pages > (int64_t)0x7fffffff / c.page_size) return false;
     const int64_t tiles = B * max_pages * c.heads * p.chunks * (c.page_size / kKvTile);
     const int64_t most = kv_tile_bytes(c.format, c.head_dim) >= 16384 ? kMaxGrid / kCtasPerSm : kMaxGrid;
-    p.grid = (tiles + 3) / 4 < most ? (tiles + 3) / 4 : most;
+    p.shape.grid = (tiles + 3) / 4 < most ? (tiles + 3) / 4 : most;
+    p.shape.seg_tiles = max_pages * (c.page_size / kKvTile);
     p.header = ((size_t)(B + 2) * 4 + 255) / 256 * 256;
-    p.bytes = p.header + (size_t)p.grid * 2 * p.cols * (c.head_dim + 2) * 4;
+    p.bytes = p.header + (size_t)p.shape.grid * 2 * p.cols * (c.head_dim + 2) * 4;
     return true;
 }
 
@@ -62,10 +63,14 @@ int launch_attn_decode(const KvView& c, const AttnDecodeLaunch& L, cudaStream_t 
     a.partial = (float*)((char*)L.ws + p.header);
     a.status = L.status;
     a.zero = 0;
+    // a window of w tokens lies in at most (w + 14) / 16 + 1 tiles
+    attn::Shape shape = p.shape;
+    if (L.window > 0 && ((int64_t)L.window + 14) / kKvTile + 1 < shape.seg_tiles)
+        shape.seg_tiles = ((int64_t)L.window + 14) / kKvTile + 1;
     switch (c.format) {
-        case NVFP4_KV_BF16: return attn::run_bf16(a, p.grid, L.y_dtype, st);
-        case NVFP4_KV_E4M3: return attn::run_e4m3(a, p.grid, L.y_dtype, st);
-        default: return attn::run_nvfp4(a, p.grid, L.y_dtype, st);
+        case NVFP4_KV_BF16: return attn::run_bf16(a, shape, L.y_dtype, st);
+        case NVFP4_KV_E4M3: return attn::run_e4m3(a, shape, L.y_dtype, st);
+        default: return attn::run_nvfp4(a, shape, L.y_dtype, st);
     }
 }
 

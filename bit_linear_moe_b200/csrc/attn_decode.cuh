@@ -64,6 +64,14 @@ struct Args {
     uint32_t zero;     // always 0 (see refill)
 };
 
+// What the host knows of a call: the grid of the even split, and the most
+// tiles a segment can have.
+struct Shape {
+    int64_t grid, seg_tiles;
+};
+// Up to this many tiles per warp a cluster per segment is used.
+constexpr int64_t kSegmentTiles = 16;
+
 // A piece: O [cols][D], then m [cols] (log2 units), then l [cols].
 template <int D, int NT>
 struct Piece {
@@ -189,6 +197,20 @@ NVFP4_DEV void seen_range(const Args& a, int b, int& lo, int& len) {
     lo = (a.window > 0 && len > a.window) ? len - a.window : 0;
 }
 
+// Where tile jt of sequence b lies, for key head hk.  A page out of range is
+// reported and page 0 read in its place.
+template <int TILE>
+NVFP4_DEV const uint8_t* tile_address(const Args& a, uint32_t b, uint32_t hk, uint32_t jt) {
+    const uint32_t per = (uint32_t)(a.c.page_size / kKvTile);
+    const uint32_t pi = (per & (per - 1)) == 0 ? jt >> (31 - __clz(per)) : jt / per;
+    int64_t page = a.table[(int64_t)b * a.table_ld + pi];
+    if (page < 0 || page >= a.c.num_pages) {
+        if (a.status) atomicExch(a.status, NVFP4_ERR_PAGE);
+        page = 0;
+    }
+    return a.c.data + ((page * a.c.heads + hk) * per + (jt - pi * per)) * TILE;
+}
+
 // Writes out[v] (eight consecutive columns) of one query head.
 NVFP4_DEV void store_y8(__nv_bfloat16* p, const float (&v)[8]) {
     *reinterpret_cast<uint4*>(p) =
@@ -198,6 +220,9 @@ NVFP4_DEV void store_y8(float* p, const float (&v)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
+
+NVFP4_DEV void store_y2(__nv_bfloat16* p, float a, float b) { *reinterpret_cast<uint32_t*>(p) = pack_b16(a, b); }
+NVFP4_DEV void store_y2(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
 
 // 1 / l, or 0 where nothing was seen (or every score is -inf).  A NaN stays.
 NVFP4_DEV float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
@@ -236,10 +261,7 @@ struct Warp {
     float m[NT][2], l[NT][2], f[NT][2];  // columns 2t, 2t + 1: maximum, sum (this thread's tokens), factor of the scores
 
     // Queries of segment (b, hk, chunk): column n = lane / 4 of each block.
-    // Quantized caches multiply in fp16: the column is prescaled by a power of
-    // two that brings its largest element to [2^14, 2^15), exact for every
-    // element within 2^31 of it; the factor undoes it.
-    NVFP4_DEV void load_q(const Args& a, int b, int hk, int chunk, float gs) {
+    NVFP4_DEV void fetch_q(const Args& a, int b, int hk, int chunk) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -255,6 +277,17 @@ struct Warp {
                     const int at = i * (kEk / 2) + 4 * e;
                     q[n][at] = w.x, q[n][at + 1] = w.y, q[n][at + 2] = w.z, q[n][at + 3] = w.w;
                 }
+        }
+    }
+
+    // Turns fetched queries into operands and starts a piece.  Quantized caches
+    // multiply in fp16: a column is prescaled by a power of two that brings its
+    // largest element to [2^14, 2^15), exact for every element within 2^31 of
+    // it; the factor of the scores undoes it.
+    NVFP4_DEV void start(const Args& a, float gs) {
+        const int t = threadIdx.x & 3;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
             float back = 1.0f;
             if constexpr (!kBf16) {
                 float amax = 0.0f;
@@ -315,9 +348,9 @@ struct Warp {
     }
 
     // Tile with tokens tok0 .. tok0 + 15; those outside [lo, len) are masked
-    // (EDGE; their bytes may be anything, NaN included).
-    template <bool EDGE>
+    // (their bytes may be anything, NaN included).
     NVFP4_DEV void tile(const uint8_t* tp, int tok0, int lo, int len) {
+        const bool edge = tok0 < lo || tok0 + kKvTile > len;
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const uint8_t* ks = tp + 32 * C::kDb;  // key scales, then value scales
         // ---- S^T = K Q^T: this thread's rows g and g + 8
@@ -394,7 +427,10 @@ struct Warp {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 x[c] = (s[n][0][c] + s[n][1][c]) * f[n][c & 1];
-                if constexpr (EDGE) {
+            }
+            if (edge) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
                     const int tok = tok0 + g + 8 * (c >> 1);
                     if (tok < lo || tok >= len) x[c] = __int_as_float(0xff800000);
                 }
@@ -464,8 +500,11 @@ struct Warp {
                     if constexpr (kUv == 16) sb[k] = *reinterpret_cast<const uint16_t*>(sp);
                     else sb[k] = *sp;
                 }
-                if constexpr (EDGE) {
-                    const int tok = tok0 + r;
+            }
+            if (edge) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int tok = tok0 + 2 * t + (k & 1) + 8 * (k >> 1);
                     if (tok < lo || tok >= len) {
 #pragma unroll
                         for (int e = 0; e < kUv / 4; ++e) w[k][e] = 0u;
@@ -514,6 +553,17 @@ struct Warp {
                     }
                 }
             }
+        }
+    }
+
+    NVFP4_DEV void scale_values(float v_gs) {
+        if constexpr (FMT != NVFP4_KV_BF16) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < C::kMt; ++k)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[n][k][c] *= v_gs;
         }
     }
 
@@ -592,6 +642,67 @@ struct Warp {
     }
 };
 
+// One column of several pieces joined by a warp; a lane holds D / 32
+// consecutive elements of the head.
+template <int D>
+struct Joined {
+    static constexpr int kV = D / 32;
+    float v[kV], M, L;
+
+    // Pieces p with bit p of `set` (p < P), at piece(p) in shared memory.
+    template <int NT, int P, typename F>
+    NVFP4_DEV void join(F piece, uint32_t set, int col) {
+        constexpr int kCols = 8 * NT;
+        const int lane = threadIdx.x & 31;
+        const bool in = lane < P && (set >> lane & 1);
+        const float* mine = piece(in ? lane : __ffs(set) - 1) + kCols * D + col;
+        const float m = in ? mine[0] : __int_as_float(0xff800000);
+        M = warp_max(m);
+        const float w = in ? weight(m, M) : 0.0f;
+        L = warp_sum(in ? w * mine[kCols] : 0.0f);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) v[k] = 0.0f;
+        const float* base = nullptr;
+#pragma unroll 4
+        for (int p = 0; p < P; ++p) {
+            if (!(set >> p & 1)) continue;
+            base = piece(p) + col * D + lane * kV;
+            const float wp = __shfl_sync(0xffffffffu, w, p);
+#pragma unroll
+            for (int k = 0; k < kV; k += 2) {
+                const float2 x = *reinterpret_cast<const float2*>(base + k);
+                v[k] += wp * x.x;
+                v[k + 1] += wp * x.y;
+            }
+        }
+    }
+
+    template <typename YT>
+    NVFP4_DEV void store_output(const Args& a, uint32_t b, uint32_t hk, int qc) const {
+        if (qc >= a.G) return;
+        const int lane = threadIdx.x & 31;
+        const int64_t row = (int64_t)b * a.q_heads + hk * a.G + qc;
+        const float inv = inverse_sum(L);
+        YT* yp = (YT*)a.y + row * D + lane * kV;
+#pragma unroll
+        for (int k = 0; k < kV; k += 2) store_y2(yp + k, v[k] * inv, v[k + 1] * inv);
+        if (a.lse && lane == 0) a.lse[row] = lse_of(M, L);
+    }
+
+    template <int NT>
+    NVFP4_DEV void store_piece(float* part, int col) const {
+        constexpr int kCols = 8 * NT;
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int k = 0; k < kV; k += 2)
+            *reinterpret_cast<float2*>(part + col * D + lane * kV + k) = make_float2(v[k], v[k + 1]);
+        if (lane == 0) {
+            part[kCols * D + col] = M;
+            part[kCols * D + kCols + col] = L;
+        }
+    }
+};
+
 template <int FMT, int D, int NT, typename YT>
 __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>::kTile >= 16384 ? 1 : kCtasPerSm)
     attn_decode_kernel(const Args a) {
@@ -602,7 +713,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
     float* pieces = reinterpret_cast<float*>(smem + C::kRingBytes);
     uint32_t* first = reinterpret_cast<uint32_t*>(smem + C::kFixed);  // [B + 1]
     __shared__ uint64_t s_full[W][S];
-    __shared__ uint32_t s_seg[2 * W], s_scan[W], s_flag;
+    __shared__ uint32_t s_seg[2 * W], s_scan[W];
+    __shared__ uint4 s_desc[2 * W];  // of a stored piece: tiles, sequence, key head, chunk
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     griddep_launch_dependents();
@@ -664,25 +776,19 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
     uint64_t* full = s_full[warp];
     float* my_first = pieces + warp * Piece<D, NT>::kFloats;
     float* my_last = reinterpret_cast<float*>(ring);
-    const uint32_t tiles_per_page = (uint32_t)(a.c.page_size / kKvTile);
     if (n_warp > 0) {
-        // addresses of tiles 32 k .. 32 k + 31, one per lane
+        // addresses of tiles i0 .. i0 + 31 of this warp, one per lane; `pl` is
+        // the place of a tile at or before them in the same segment
         const uint8_t* addr = nullptr;
-        auto look_up = [&](uint32_t i0) {
+        auto look_up = [&](uint32_t i0, const Place& pl, uint32_t pl_i) {
             const uint32_t i = i0 + lane;
             if (i < n_warp) {
-                const Place p = place_of(w0 + i, hc, first, B);
+                Place p = pl;
+                p.j += i - pl_i;
+                if (p.j >= p.tiles) p = place_of(w0 + i, hc, first, B);
                 int lo, len;
                 seen_range(a, (int)p.b, lo, len);
-                const uint32_t jt = (uint32_t)(lo / kKvTile) + p.j;
-                const uint32_t pi = jt / tiles_per_page;
-                int64_t page = a.table[(int64_t)p.b * a.table_ld + pi];
-                if (page < 0 || page >= a.c.num_pages) {  // reported; page 0 is read in its place
-                    if (a.status) atomicExch(a.status, NVFP4_ERR_PAGE);
-                    page = 0;
-                }
-                const uint32_t hk = p.s / (uint32_t)a.chunks;
-                addr = a.c.data + ((page * a.c.heads + hk) * tiles_per_page + (jt - pi * tiles_per_page)) * C::kTile;
+                addr = tile_address<C::kTile>(a, p.b, p.s / (uint32_t)a.chunks, (uint32_t)(lo / kKvTile) + p.j);
             }
         };
         // `dep` is made of registers that hold the results of everything read
@@ -695,31 +801,25 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
                 bulk_load(ring + slot * C::kTile, addr, bytes, &full[slot]);
             }
         };
-        look_up(0);
-        for (uint32_t i = 0; i < (uint32_t)S; ++i) refill(i, i, 0u);
-
+        Place at = place_of(w0, hc, first, B);
+        uint32_t hk = at.s / (uint32_t)a.chunks, chunk = at.s - hk * (uint32_t)a.chunks;
         Warp<FMT, D, NT, YT> wk;
+        wk.fetch_q(a, (int)at.b, (int)hk, (int)chunk);  // on their way while the page table is read
+        look_up(0, at, 0);
+        for (uint32_t i = 0; i < (uint32_t)S; ++i) refill(i, i, 0u);
         float k_gs = 1.0f;
         float v_gs = 1.0f;
         if constexpr (FMT != NVFP4_KV_BF16) {
             k_gs = *a.c.k_gs;
             v_gs = *a.c.v_gs;
         }
-        Place at = place_of(w0, hc, first, B);
-        int lo = 0, len = 0, tok0 = 0;
+        int lo, len;
+        seen_range(a, (int)at.b, lo, len);
+        int tok0 = (lo / kKvTile + (int)at.j) * kKvTile;
         uint32_t begun = at.j;  // tile of the segment this piece starts with
-        uint32_t hk = 0, chunk = 0, slot = 0, phase = 0;
-        bool fresh = true;
+        uint32_t slot = 0, phase = 0;
+        wk.start(a, k_gs);
         for (uint32_t i = 0; i < n_warp; ++i) {
-            if (fresh) {
-                seen_range(a, (int)at.b, lo, len);
-                tok0 = (lo / kKvTile + (int)at.j) * kKvTile;
-                hk = at.s / (uint32_t)a.chunks;
-                chunk = at.s - hk * (uint32_t)a.chunks;
-                wk.load_q(a, (int)at.b, (int)hk, (int)chunk, k_gs);
-                begun = at.j;
-                fresh = false;
-            }
             const bool ok = mbar_wait(&full[slot], phase, a.status);
             if (!__all_sync(0xffffffffu, ok)) {
                 // a copy that never arrived: wait (again bounded) for the others and stop
@@ -727,106 +827,196 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
                 break;
             }
             const uint8_t* tp = ring + slot * C::kTile;
-            if (tok0 >= lo && tok0 + kKvTile <= len) wk.template tile<false>(tp, tok0, lo, len);
-            else wk.template tile<true>(tp, tok0, lo, len);
+            wk.tile(tp, tok0, lo, len);
             const uint32_t next = i + S;
-            if ((next & 31) == 0) look_up(next);
+            if ((next & 31) == 0) look_up(next, at, i);
             refill(next, slot, wk.depend());
             tok0 += kKvTile;
             if (++slot == (uint32_t)S) slot = 0, phase ^= 1;
             // ---- end of the segment or of the range
             const bool ends = at.j + 1 == at.tiles;
             if (ends || i + 1 == n_warp) {
-                // the values' global scale
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int k = 0; k < C::kMt; ++k)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if constexpr (FMT != NVFP4_KV_BF16) wk.o[n][k][c] *= v_gs;
+                wk.scale_values(v_gs);
                 if (ends && begun == 0) {
                     wk.store_output(a, (int)at.b, (int)hk, (int)chunk);
                 } else {
                     const uint32_t id = first[at.b] * hc + at.s * at.tiles;  // the segment's first tile names it
                     wk.store_piece(ends ? my_first : my_last);
-                    if (lane == 0) s_seg[2 * warp + (ends ? 0 : 1)] = id;
+                    if (lane == 0) {
+                        s_seg[2 * warp + (ends ? 0 : 1)] = id;
+                        s_desc[2 * warp + (ends ? 0 : 1)] = make_uint4(at.tiles, at.b, hk, chunk);
+                    }
                 }
-                fresh = true;
             }
-            if (!ends) {
-                ++at.j;
-            } else {
-                at.j = 0;
+            ++at.j;
+            if (ends && i + 1 < n_warp) {  // the next segment
+                at.j = begun = 0;
                 if (++at.s == hc) {
                     at.s = 0;
                     do ++at.b;
-                    while (at.b < B && first[at.b + 1] == first[at.b]);
-                    if (at.b < B) at.tiles = first[at.b + 1] - first[at.b];
+                    while (first[at.b + 1] == first[at.b]);
+                    at.tiles = first[at.b + 1] - first[at.b];
                 }
+                hk = at.s / (uint32_t)a.chunks;
+                chunk = at.s - hk * (uint32_t)a.chunks;
+                wk.fetch_q(a, (int)at.b, (int)hk, (int)chunk);
+                seen_range(a, (int)at.b, lo, len);
+                tok0 = lo / kKvTile * kKvTile;
+                wk.start(a, k_gs);
             }
         }
     }
     __syncthreads();
 
-    // ---- segments that several warps share, in list order
-    for (int p0 = 0; p0 < 2 * W;) {
-        const uint32_t id = s_seg[p0];
-        if (id == 0xffffffffu) {
-            ++p0;
-            continue;
-        }
-        int p1 = p0 + 1;  // pieces p0 .. p1 - 1 of segment `id` (absent ones in between)
-        for (int p = p1; p < 2 * W; ++p) {
-            if (s_seg[p] == id) p1 = p + 1;
-            else if (s_seg[p] != 0xffffffffu) break;
-        }
-        const Place at = place_of(id, hc, first, B);
-        const uint32_t hk = at.s / (uint32_t)a.chunks, chunk = at.s - hk * (uint32_t)a.chunks;
-        const bool whole = id >= t0 && id + at.tiles <= t1;
-        float* part = a.partial + ((int64_t)blockIdx.x * 2 + (id >= t0 ? 1 : 0)) * Piece<D, NT>::kFloats;
-        auto piece = [&](int p) -> const float* {
-            return (p & 1) ? reinterpret_cast<const float*>(ring_all + (size_t)(p >> 1) * S * C::kTile)
-                           : pieces + (p >> 1) * Piece<D, NT>::kFloats;
-        };
-        for (int e = threadIdx.x; e < kCols * (D / 8); e += W * 32) {
-            const int col = e / (D / 8), d = (e % (D / 8)) * 8;
-            float M = __int_as_float(0xff800000);
-            for (int p = p0; p < p1; ++p)
-                if (s_seg[p] == id) M = fmaxf(M, piece(p)[kCols * D + col]);
-            float v[8], L = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-            for (int p = p0; p < p1; ++p) {
-                if (s_seg[p] != id) continue;
-                const float* src = piece(p);
-                const float w = weight(src[kCols * D + col], M);
-                L += w * src[kCols * D + kCols + col];
-                const float4 x = *reinterpret_cast<const float4*>(src + col * D + d);
-                const float4 y = *reinterpret_cast<const float4*>(src + col * D + d + 4);
-                v[0] += w * x.x, v[1] += w * x.y, v[2] += w * x.z, v[3] += w * x.w;
-                v[4] += w * y.x, v[5] += w * y.y, v[6] += w * y.z, v[7] += w * y.w;
-            }
-            if (whole) {
-                const int qc = (int)chunk * kCols + col;
-                if (qc < a.G) {
-                    const int64_t row = (int64_t)at.b * a.q_heads + hk * a.G + qc;
-                    const float inv = inverse_sum(L);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] *= inv;
-                    store_y8((YT*)a.y + row * D + d, v);
-                    if (a.lse && d == 0) a.lse[row] = lse_of(M, L);
-                }
-            } else {
-                store_y8(part + col * D + d, v);
-                if (d == 0) {
-                    part[kCols * D + col] = M;
-                    part[kCols * D + kCols + col] = L;
-                }
-            }
-        }
-        p0 = p1;
+    // ---- segments that several warps share: a warp per (segment, column)
+    const uint32_t my_seg = lane < 2 * W ? s_seg[lane] : 0xffffffffu;
+    const uint32_t same = __match_any_sync(0xffffffffu, my_seg);
+    const bool leads = my_seg != 0xffffffffu && (same & ((1u << lane) - 1)) == 0;
+    const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+    const int rank = __popc(leaders & ((1u << lane) - 1));
+    const int tasks = __popc(leaders) * kCols;
+    auto piece = [&](int p) -> const float* {  // the warp's first (even) or, in its ring, its last (odd)
+        return (p & 1) ? reinterpret_cast<const float*>(ring_all + (size_t)(p >> 1) * S * C::kTile)
+                       : pieces + (p >> 1) * Piece<D, NT>::kFloats;
+    };
+    for (int task = warp; task < tasks; task += W) {
+        const int col = task % kCols, lead = __ffs(__ballot_sync(0xffffffffu, leads && rank == task / kCols)) - 1;
+        const uint32_t id = __shfl_sync(0xffffffffu, my_seg, lead), set = __shfl_sync(0xffffffffu, same, lead);
+        const uint4 ds = s_desc[lead];
+        Joined<D> r;
+        r.template join<NT, 2 * W>(piece, set, col);
+        if (id >= t0 && id + ds.x <= t1) r.template store_output<YT>(a, ds.y, ds.z, ds.w * kCols + col);
+        else r.template store_piece<NT>(a.partial + ((int64_t)blockIdx.x * 2 + (id >= t0 ? 1 : 0)) * Piece<D, NT>::kFloats, col);
     }
+}
+
+// The same for few tiles per warp (short contexts, few sequences), where the
+// latencies of the list, of shared segments and of a second kernel weigh more
+// than an even split: a cluster of CTAs takes one segment, each an equal
+// contiguous range of its tiles, and joins it through distributed shared
+// memory.  No workspace.
+template <int FMT, int D, int NT, typename YT>
+__global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>::kTile >= 16384 ? 1 : kCtasPerSm)
+    attn_segment_kernel(const Args a, const int cluster) {
+    using C = Cfg<FMT, D, NT>;
+    constexpr int W = C::kWarps, S = C::kRing, kCols = 8 * NT;
+    extern __shared__ __align__(128) uint8_t smem[];
+    float* joined = reinterpret_cast<float*>(smem + C::kRingBytes);  // this CTA's piece
+    __shared__ uint64_t s_full[W][S];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t seg = blockIdx.x / (uint32_t)cluster, rank = blockIdx.x - seg * (uint32_t)cluster;
+    const uint32_t hc = (uint32_t)(a.c.heads * a.chunks);
+    const uint32_t b = seg / hc, s = seg - b * hc, hk = s / (uint32_t)a.chunks, chunk = s - hk * (uint32_t)a.chunks;
+    uint8_t* ring = smem + (size_t)warp * S * C::kTile;
+    uint64_t* full = s_full[warp];
+
+    griddep_launch_dependents();
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(&full[i], 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
+    griddep_wait();
+    Warp<FMT, D, NT, YT> wk;
+    wk.fetch_q(a, (int)b, (int)hk, (int)chunk);
+    float k_gs = 1.0f, v_gs = 1.0f;
+    if constexpr (FMT != NVFP4_KV_BF16) {
+        k_gs = *a.c.k_gs;
+        v_gs = *a.c.v_gs;
+    }
+    int lo, len;
+    seen_range(a, (int)b, lo, len);
+    if (a.lens[b] > len && a.lens[b] > 0 && a.status) atomicExch(a.status, NVFP4_ERR_PAGE);
+    const uint32_t j_first = (uint32_t)(lo / kKvTile);
+    const uint32_t tiles = len > lo ? (uint32_t)((len + kKvTile - 1) / kKvTile) - j_first : 0u;
+    // warp `rank * W + warp` of cluster * W takes an equal range
+    const uint32_t parts = (uint32_t)(cluster * W), part = rank * W + warp;
+    const uint32_t each = tiles / parts, more = tiles - each * parts;
+    const uint32_t n_warp = each + (part < more ? 1u : 0u);
+    const uint32_t j0 = j_first + each * part + min(part, more);
+
+    const uint8_t* addr = nullptr;
+    auto look_up = [&](uint32_t i0) {
+        if (i0 + lane < n_warp) addr = tile_address<C::kTile>(a, b, hk, j0 + i0 + lane);
+    };
+    auto refill = [&](uint32_t i, uint32_t slot, uint32_t dep) {  // as in attn_decode_kernel
+        if (i < n_warp && lane == (int)(i & 31)) {
+            const uint32_t bytes = (uint32_t)C::kTile + (dep & a.zero);
+            mbar_expect_tx(&full[slot], bytes);
+            bulk_load(ring + slot * C::kTile, addr, bytes, &full[slot]);
+        }
+    };
+    look_up(0);
+    for (uint32_t i = 0; i < (uint32_t)S; ++i) refill(i, i, 0u);
+    wk.start(a, k_gs);
+    uint32_t slot = 0, phase = 0;
+    int tok0 = (int)j0 * kKvTile;
+    for (uint32_t i = 0; i < n_warp; ++i) {
+        const bool ok = mbar_wait(&full[slot], phase, a.status);
+        if (!__all_sync(0xffffffffu, ok)) {
+            for (uint32_t k = i + 1; k < i + S && k < n_warp; ++k) mbar_wait(&full[k % S], (k / S) & 1, a.status);
+            break;
+        }
+        wk.tile(ring + slot * C::kTile, tok0, lo, len);
+        const uint32_t next = i + S;
+        if ((next & 31) == 0) look_up(next);
+        refill(next, slot, wk.depend());
+        tok0 += kKvTile;
+        if (++slot == (uint32_t)S) slot = 0, phase ^= 1;
+    }
+    wk.scale_values(v_gs);
+    wk.store_piece(reinterpret_cast<float*>(ring));
+    __syncthreads();
+
+    auto piece = [&](int p) -> const float* {
+        return reinterpret_cast<const float*>(smem + (size_t)p * S * C::kTile);
+    };
+    const uint32_t set = (1u << W) - 1;
+    if (cluster == 1) {
+        for (int col = warp; col < kCols; col += W) {
+            Joined<D> r;
+            r.template join<NT, W>(piece, set, col);
+            r.template store_output<YT>(a, b, hk, (int)chunk * kCols + col);
+        }
+        return;
+    }
+    for (int col = warp; col < kCols; col += W) {
+        Joined<D> r;
+        r.template join<NT, W>(piece, set, col);
+        r.template store_piece<NT>(joined, col);
+    }
+    cluster_sync();
+    // the cluster's CTAs share the columns; a lane reads its elements of every
+    // CTA's piece
+    for (int col = (int)rank + cluster * warp; col < kCols; col += cluster * W) {
+        Joined<D> r;
+        float m[8], l[8];
+        r.M = __int_as_float(0xff800000);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            m[c] = __int_as_float(0xff800000);
+            l[c] = 0.0f;
+            if (c < cluster) {
+                m[c] = ld_dsmem_f32(joined + kCols * D + col, (uint32_t)c);
+                l[c] = ld_dsmem_f32(joined + kCols * D + kCols + col, (uint32_t)c);
+            }
+            r.M = fmaxf(r.M, m[c]);
+        }
+        r.L = 0.0f;
+#pragma unroll
+        for (int k = 0; k < Joined<D>::kV; ++k) r.v[k] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            if (c >= cluster) break;
+            const float w = weight(m[c], r.M);
+            r.L += w * l[c];
+#pragma unroll
+            for (int k = 0; k < Joined<D>::kV; ++k)
+                r.v[k] += w * ld_dsmem_f32(joined + col * D + lane * Joined<D>::kV + k, (uint32_t)c);
+        }
+        r.template store_output<YT>(a, b, hk, (int)chunk * kCols + col);
+    }
+    cluster_sync();  // pieces stay until every CTA has read them
 }
 
 // Joins the segments that several CTAs share and writes zeros for sequences
@@ -894,40 +1084,60 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const Args a) {
     if (a.lse && lane == 0) a.lse[row] = lse_of(M, L);
 }
 
+// Dynamic shared memory above 48 KB is allowed once per kernel and device.
+template <typename K>
+static bool allow_smem(K kern, std::atomic<uint64_t>& done, int bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (done.load(std::memory_order_relaxed) >> dev & 1) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return true;
+}
+
 template <int FMT, int D, int NT, typename YT>
-static int run(const Args& a, int64_t grid, cudaStream_t st) {
+static int run(const Args& a, const Shape& sh, cudaStream_t st) {
     using C = Cfg<FMT, D, NT>;
-    struct Once {  // one flag per instantiation and device
-        static int set(int bytes) {
-            static std::atomic<uint64_t> done{0};
-            int dev = 0;
-            if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return NVFP4_ERR_LAUNCH;
-            if (done.load(std::memory_order_relaxed) >> dev & 1) return NVFP4_OK;
-            if (cudaFuncSetAttribute(attn_decode_kernel<FMT, D, NT, YT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     bytes) != cudaSuccess)
-                return NVFP4_ERR_LAUNCH;
-            done.fetch_or(1ull << dev, std::memory_order_relaxed);
-            return NVFP4_OK;
-        }
-    };
-    constexpr int kMostB = 4096;
-    NVFP4_TRY_INTERNAL(Once::set(C::kFixed + (kMostB + 4) * 4));
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     set_pdl_attr(attr[0]);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(C::kWarps * 32);
-    cfg.dynamicSmemBytes = (size_t)C::kFixed + (size_t)((a.B + 4) / 4 * 4) * 4 + 16;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    // One cluster per segment: as many CTAs as leave every segment its own
+    // (8 at most, the portable size), no more than give a warp one tile.
+    const int64_t segments = (int64_t)a.B * a.c.heads * a.chunks;
+    const int64_t slots = C::kTile >= 16384 ? kMaxGrid / kCtasPerSm : kMaxGrid;
+    int64_t cluster = slots / segments, most = (sh.seg_tiles + C::kWarps - 1) / C::kWarps;
+    cluster = cluster < 1 ? 1 : cluster > 8 ? 8 : cluster;
+    if (cluster > most) cluster = most;
+    if (sh.seg_tiles <= cluster * C::kWarps * kSegmentTiles) {
+        static std::atomic<uint64_t> done{0};
+        constexpr int bytes = C::kRingBytes + C::kPieceBytes;
+        if (!allow_smem(attn_segment_kernel<FMT, D, NT, YT>, done, bytes)) return NVFP4_ERR_LAUNCH;
+        cfg.gridDim = dim3((unsigned)(segments * cluster));
+        cfg.dynamicSmemBytes = bytes;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, attn_segment_kernel<FMT, D, NT, YT>, a, (int)cluster) == cudaSuccess
+                   ? NVFP4_OK
+                   : NVFP4_ERR_LAUNCH;
+    }
+    static std::atomic<uint64_t> done{0};
+    constexpr int kMostB = 4096;
+    if (!allow_smem(attn_decode_kernel<FMT, D, NT, YT>, done, C::kFixed + (kMostB + 4) * 4 + 16)) return NVFP4_ERR_LAUNCH;
+    cfg.gridDim = dim3((unsigned)sh.grid);
+    cfg.dynamicSmemBytes = (size_t)C::kFixed + (size_t)((a.B + 4) / 4 * 4) * 4 + 16;
     if (cudaLaunchKernelEx(&cfg, attn_decode_kernel<FMT, D, NT, YT>, a) != cudaSuccess) return NVFP4_ERR_LAUNCH;
     // the join: a warp per row, or a CTA per row where rows may have many pieces
     const int64_t rows = (int64_t)a.B * a.q_heads;
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     cudaError_t e;
-    if ((int64_t)a.B * a.c.heads * a.chunks * 8 > grid) {
+    if (segments * 8 > sh.grid) {
         cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
         e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D, NT, YT, 8>, a);
     } else {
@@ -942,12 +1152,12 @@ static int run(const Args& a, int64_t grid, cudaStream_t st) {
 constexpr int cols_of(int G, int D) { return (G > 8 && D <= 128) ? 16 : 8; }
 
 template <int FMT, typename YT>
-static int run_fmt(const Args& a, int64_t grid, cudaStream_t st) {
+static int run_fmt(const Args& a, const Shape& sh, cudaStream_t st) {
     const bool two = cols_of(a.G, a.c.head_dim) == 16;
     switch (a.c.head_dim) {
-        case 64: return two ? run<FMT, 64, 2, YT>(a, grid, st) : run<FMT, 64, 1, YT>(a, grid, st);
-        case 128: return two ? run<FMT, 128, 2, YT>(a, grid, st) : run<FMT, 128, 1, YT>(a, grid, st);
-        case 256: return run<FMT, 256, 1, YT>(a, grid, st);
+        case 64: return two ? run<FMT, 64, 2, YT>(a, sh, st) : run<FMT, 64, 1, YT>(a, sh, st);
+        case 128: return two ? run<FMT, 128, 2, YT>(a, sh, st) : run<FMT, 128, 1, YT>(a, sh, st);
+        case 256: return run<FMT, 256, 1, YT>(a, sh, st);
         default: return NVFP4_ERR_SHAPE;
     }
 }

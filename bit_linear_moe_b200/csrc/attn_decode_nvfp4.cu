@@ -5,8 +5,8 @@
 namespace nvfp4 {
 namespace attn {
 
-int run_nvfp4(const Args& a, int64_t grid, int y_dtype, cudaStream_t st) {
-    return y_dtype == NVFP4_DTYPE_BF16 ? run_fmt<NVFP4_KV_NVFP4, __nv_bfloat16>(a, grid, st) : run_fmt<NVFP4_KV_NVFP4, float>(a, grid, st);
+int run_nvfp4(const Args& a, const Shape& sh, int y_dtype, cudaStream_t st) {
+    return y_dtype == NVFP4_DTYPE_BF16 ? run_fmt<NVFP4_KV_NVFP4, __nv_bfloat16>(a, sh, st) : run_fmt<NVFP4_KV_NVFP4, float>(a, sh, st);
 }
 
 }  // namespace attn

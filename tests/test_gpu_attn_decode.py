@@ -92,30 +92,36 @@ class Batch:
 
 
 LENS = (0, 1, 2, 15, 16, 17, 31, 48, 100, 129)
+# The host knows lengths only by the table's width: a narrow table is served by a cluster
+# of CTAs per (sequence, key head), a wide one by an even split of all tiles.
+WIDE = 600
+WIDTHS = pytest.mark.parametrize("extra", [0, WIDE], ids=["narrow", "wide"])
 
 
+@WIDTHS
 @pytest.mark.parametrize("y_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("fmt", FMTS)
-def test_lengths_around_tiles_and_pages(cuda_device, fmt, D, y_dtype):
-    b = Batch(fmt, D, 2, 4, 32, LENS)
+def test_lengths_around_tiles_and_pages(cuda_device, fmt, D, y_dtype, extra):
+    b = Batch(fmt, D, 2, 4, 32, LENS, extra_cols=extra)
     y, lse = b.run(y_dtype=y_dtype)
     b.check(y, lse)
     assert nv.nvfp4_read_device_status() == nv.OK
 
 
+@WIDTHS
 @pytest.mark.parametrize("G", [1, 2, 3, 5, 8, 9, 16, 17, 33])
 @pytest.mark.parametrize("fmt,D", [(oat.NVFP4, 128), (oat.NVFP4, 256), (oat.E4M3, 64), (oat.BF16, 128)])
-def test_query_heads_per_key_head(cuda_device, fmt, D, G):
-    b = Batch(fmt, D, 3, G, 16, (37, 200, 5))
+def test_query_heads_per_key_head(cuda_device, fmt, D, G, extra):
+    b = Batch(fmt, D, 3, G, 16, (37, 200, 5), extra_cols=extra)
     b.check(*b.run())
 
 
 @pytest.mark.parametrize("fmt,D,page", [(oat.NVFP4, 128, 48), (oat.NVFP4, 64, 256), (oat.E4M3, 128, 16),
                                         (oat.BF16, 256, 64)])
-@pytest.mark.parametrize("window", [1, 16, 40, 1000])
-def test_window(cuda_device, fmt, D, page, window):
-    b = Batch(fmt, D, 2, 2, page, (0, 1, 16, 41, 300, 513))
+@pytest.mark.parametrize("window,extra", [(1, 0), (16, 0), (40, 0), (1000, 0), (5000, WIDE)])
+def test_window(cuda_device, fmt, D, page, window, extra):
+    b = Batch(fmt, D, 2, 2, page, (0, 1, 16, 41, 300, 513, 5300), extra_cols=extra)
     b.check(*b.run(window=window), window=window)
 
 
@@ -123,20 +129,22 @@ def test_window(cuda_device, fmt, D, page, window):
 @pytest.mark.parametrize("D,Hkv,G,lens", [
     (128, 1, 8, (9001,)), (128, 2, 2, (4097, 33)), (64, 1, 16, (20000,)), (256, 1, 3, (6000, 0, 700)),
     (128, 4, 2, tuple(int(x) for x in np.random.default_rng(2).integers(0, 700, 60)))])
-def test_work_split_over_ctas(cuda_device, fmt, D, Hkv, G, lens):
+@WIDTHS
+def test_work_split_over_ctas(cuda_device, fmt, D, Hkv, G, lens, extra):
     """Long sequences over many CTAs, and ragged batches whose segments end anywhere in a
     CTA's or a warp's range; fp32 output shows a join that lost or doubled a piece."""
-    b = Batch(fmt, D, Hkv, G, 64, lens)
+    b = Batch(fmt, D, Hkv, G, 64, lens, extra_cols=extra)
     y, lse = b.run(y_dtype=torch.float32)
     b.check(y, lse)
     y2, lse2 = b.run(y_dtype=torch.float32)
     assert torch.equal(y, y2) and torch.equal(lse, lse2)         # the same bits
 
 
+@WIDTHS
 @pytest.mark.parametrize("fmt", FMTS)
-def test_sharp_and_flat_scores(cuda_device, fmt):
+def test_sharp_and_flat_scores(cuda_device, fmt, extra):
     """Large keys (one token takes almost all weight, the maximum rises often) and scale 0."""
-    b = Batch(fmt, 128, 2, 4, 16, (700, 64), k_scale=30.0)
+    b = Batch(fmt, 128, 2, 4, 16, (700, 64), k_scale=30.0, extra_cols=extra)
     b.check(*b.run())
     b.check(*b.run(scale=0.0), scale=0.0)
     b.check(*b.run(scale=-0.05), scale=-0.05)
@@ -159,8 +167,9 @@ def test_queries_of_unequal_size(cuda_device):
     assert torch.isfinite(y[:, 3]).all()                         # one token has all the weight
 
 
-def test_nan_and_infinity_stay_where_they_are(cuda_device):
-    b = Batch(oat.BF16, 128, 2, 2, 16, (40, 40, 40))
+@WIDTHS
+def test_nan_and_infinity_stay_where_they_are(cuda_device, extra):
+    b = Batch(oat.BF16, 128, 2, 2, 16, (40, 40, 40), extra_cols=extra)
     base, base_lse = b.run()
     b.q = b.q.clone()
     b.q[1, 2] = float("nan")
@@ -194,11 +203,12 @@ def test_shared_pages_and_table_views(cuda_device):
     b.check(*b.run())
 
 
-def test_bad_pages_and_lengths_are_reported(cuda_device):
+@WIDTHS
+def test_bad_pages_and_lengths_are_reported(cuda_device, extra):
     """Indexes out of range are caught by the kernel's own check (page 0 is read in their
     place, lengths are cut to the table) and named in the status word; other sequences
     are right."""
-    b = Batch(oat.NVFP4, 128, 2, 4, 16, (64, 80, 64))
+    b = Batch(oat.NVFP4, 128, 2, 4, 16, (64, 80, 64), extra_cols=extra)
     b.dtable[1, 2] = 1 << 20
     y, lse = b.run()
     assert nv.nvfp4_read_device_status() == nv.ERR_PAGE
@@ -217,8 +227,9 @@ def test_bad_pages_and_lengths_are_reported(cuda_device):
     b.check(y, lse, seqs=(0, 2))
 
 
-def test_nothing_outside_the_outputs_is_written(cuda_device):
-    b = Batch(oat.E4M3, 64, 2, 3, 16, (0, 130, 7))
+@WIDTHS
+def test_nothing_outside_the_outputs_is_written(cuda_device, extra):
+    b = Batch(oat.E4M3, 64, 2, 3, 16, (0, 130, 7), extra_cols=extra)
     before = b.c.data.clone()
     need = nv.nvfp4_attn_decode_workspace(b.c, 3, 6, b.table.shape[1])
     room = torch.full((need + 512,), 0xAB, dtype=torch.uint8, device="cuda")
@@ -230,18 +241,21 @@ def test_nothing_outside_the_outputs_is_written(cuda_device):
     assert torch.equal(b.c.data, before)
 
 
-def test_large_batch(cuda_device):
+@WIDTHS
+def test_large_batch(cuda_device, extra):
     """More sequences than threads in a CTA (the list is scanned in pieces)."""
     lens = [int(x) for x in np.random.default_rng(4).integers(0, 40, 1500)]
-    b = Batch(oat.NVFP4, 64, 1, 2, 16, lens)
+    b = Batch(oat.NVFP4, 64, 1, 2, 16, lens, extra_cols=extra)
     y, lse = b.run()
     b.check(y, lse, seqs=list(range(0, 1500, 37)) + [0, 255, 256, 511, 512, 1499])
 
 
-def test_captured_graphs_share_a_workspace(cuda_device):
+@WIDTHS
+def test_captured_graphs_share_a_workspace(cuda_device, extra):
     """Two captured calls with one workspace, replayed in turn on lengths that change on
     the device between replays."""
-    a, c = Batch(oat.NVFP4, 128, 2, 4, 16, (600, 33), seed=1), Batch(oat.BF16, 64, 1, 3, 32, (90, 1, 500), seed=2)
+    a = Batch(oat.NVFP4, 128, 2, 4, 16, (600, 33), seed=1, extra_cols=extra)
+    c = Batch(oat.BF16, 64, 1, 3, 32, (90, 1, 500), seed=2, extra_cols=extra)
     n = max(nv.nvfp4_attn_decode_workspace(x.c, len(x.lens), x.Hkv * x.G, x.table.shape[1]) for x in (a, c))
     ws = torch.empty(n, dtype=torch.uint8, device="cuda")
     for x in (a, c):
@@ -265,9 +279,11 @@ def test_captured_graphs_share_a_workspace(cuda_device):
             x.check(y, lse)
 
 
-def test_two_streams_at_once(cuda_device):
+@WIDTHS
+def test_two_streams_at_once(cuda_device, extra):
     """Concurrent calls with workspaces of their own."""
-    a, c = Batch(oat.NVFP4, 128, 4, 4, 16, (2000, 900), seed=1), Batch(oat.E4M3, 128, 4, 2, 32, (1500, 3000), seed=2)
+    a = Batch(oat.NVFP4, 128, 4, 4, 16, (2000, 900), seed=1, extra_cols=extra)
+    c = Batch(oat.E4M3, 128, 4, 2, 32, (1500, 3000), seed=2, extra_cols=extra)
     ref = [x.run() for x in (a, c)]
     torch.cuda.synchronize()
     s = [torch.cuda.Stream(), torch.cuda.Stream()]
