@@ -93,6 +93,10 @@ struct Cfg {
     static constexpr int kPieceBytes = Piece<D, NT>::kFloats * 4;
     static constexpr int kFixed = kRingBytes + kWarps * kPieceBytes;  // then the prefix
     static constexpr int kMt = D / 16;                                 // 16-row tiles of O^T
+    // Tiles a warp works on at a time.  Two where the codes are converted
+    // (about 450 instructions a tile): their chains interleave and share the
+    // softmax's exchange and the loop.
+    static constexpr int kStep = FMT == NVFP4_KV_NVFP4 && kRing >= 4 ? 2 : 1;
     static_assert(kRing >= 2, "one tile in flight while one is used");
     static_assert(kRing * kTile >= kPieceBytes, "a warp's last piece goes into its ring");
 };
@@ -133,25 +137,6 @@ NVFP4_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, ui
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Codes to fp16 without the conversion unit (16 lanes per clock and SM, which
-// alone would hold NVFP4 at 0.7 of the memory's rate): an E2M1 code's exponent
-// and mantissa bits put at the top of fp16's mantissa and the bottom of its
-// exponent are the value times 2^-14, subnormals included; E4M3's likewise,
-// times 2^-8.
-// Eight E2M1 codes -> four pairs (i, i + 4) of value * 2^-14.
-NVFP4_DEV void e2m1x8_to_f16x2_bits(uint32_t w, uint32_t (&h)[4]) {
-    h[0] = ((w << 12) & 0x80008000u) | ((w << 9) & 0x0E000E00u);
-    h[1] = ((w << 8) & 0x80008000u) | ((w << 5) & 0x0E000E00u);
-    h[2] = ((w << 4) & 0x80008000u) | ((w << 1) & 0x0E000E00u);
-    h[3] = (w & 0x80008000u) | ((w >> 3) & 0x0E000E00u);
-}
-// Four E4M3 codes -> pairs (0, 1) and (2, 3) of value * 2^-8 (no NaN codes).
-NVFP4_DEV void e4m3x4_to_f16x2_bits(uint32_t w, uint32_t& h0, uint32_t& h1) {
-    const uint32_t a = prmt(w, 0u, 0x1404), b = prmt(w, 0u, 0x3424);
-    h0 = (a & 0x80008000u) | ((a >> 1) & 0x3F803F80u);
-    h1 = (b & 0x80008000u) | ((b >> 1) & 0x3F803F80u);
 }
 
 // N bytes (4, 8 or 16) of shared memory as words.
@@ -250,11 +235,6 @@ struct Warp {
     static constexpr int kPerByteX2 = FMT == NVFP4_KV_BF16 ? 1 : FMT == NVFP4_KV_E4M3 ? 2 : 4;  // elements per 2 bytes
     static constexpr int kEk = kUk * kPerByteX2 / 2, kEv = kUv * kPerByteX2 / 2;                // elements per unit
     static constexpr int kQw = D / 8;  // query words of a thread per column block
-    // NVFP4 key words of a unit that are converted with bit operations (the
-    // others and the values use the conversion unit): balances the two.
-    static constexpr int kBitsFrom = 1;
-    // what the key products come out divided by (bit conversions)
-    static constexpr float kUp = FMT == NVFP4_KV_NVFP4 ? 128.0f : FMT == NVFP4_KV_E4M3 ? 256.0f : 1.0f;
 
     uint32_t q[NT][kQw];
     float o[NT][C::kMt][4];
@@ -304,20 +284,11 @@ struct Warp {
                 for (int i = 0; i < kQw; ++i)
                     q[n][i] = pack_f16(bf16lo_to_f32(q[n][i]) * up, bf16hi_to_f32(q[n][i]) * up);
             }
-            if constexpr (FMT == NVFP4_KV_NVFP4) {  // words of bit-converted keys pair elements i, i + 4
-#pragma unroll
-                for (int i = 0; i < kQw; i += 4)
-                    if ((i / 4) % (kUk / 4) >= kBitsFrom) {
-                        const uint32_t a0 = q[n][i], a1 = q[n][i + 1], a2 = q[n][i + 2], a3 = q[n][i + 3];
-                        q[n][i] = prmt(a0, a2, 0x5410), q[n][i + 1] = prmt(a0, a2, 0x7632);
-                        q[n][i + 2] = prmt(a1, a3, 0x5410), q[n][i + 3] = prmt(a1, a3, 0x7632);
-                    }
-            }
             // the factors of this thread's two score columns
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const float bk = __shfl_sync(0xffffffffu, back, (2 * t + c) * 4);
-                f[n][c] = a.scale_log2 * gs * bk * kUp;
+                f[n][c] = a.scale_log2 * gs * bk;
                 m[n][c] = __int_as_float(0xff800000);
                 l[n][c] = 0.0f;
             }
@@ -328,32 +299,102 @@ struct Warp {
         }
     }
 
-    // Scales of one key row's block(s) of a unit: fp16 pairs of scale * 2^-7 for
-    // the converted word(s) and scale * 2^7 for the bit-converted ones, so that
-    // both products are value * scale * 2^-7 (exact: all of E2M1 x E4M3 times
-    // 2^-7 is a multiple of 2^-17 below 2^5 with 6 significant bits).
-    struct KeyScale {
-        uint32_t lo0, hi[2];
-    };
-    static NVFP4_DEV KeyScale key_scale(const uint8_t* p) {
+    // Block scale bytes of a key row's unit -> fp16 pairs (s, s), one per block.
+    static NVFP4_DEV void key_scale(const uint8_t* p, uint32_t (&sc)[2]) {
         uint32_t h;
-        KeyScale k;
         if constexpr (kUk == 16) h = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(p));
         else h = e4m3x2_to_f16x2(*p);
-        const uint32_t up = mul_f16x2(h, 0x58005800u);  // 2^7
-        k.lo0 = mul_f16x2(prmt(h, h, 0x1010), 0x20002000u);  // 2^-7
-        k.hi[0] = prmt(up, up, 0x1010);
-        k.hi[1] = prmt(up, up, 0x3232);
-        return k;
+        sc[0] = prmt(h, h, 0x1010);
+        sc[1] = prmt(h, h, 0x3232);
     }
 
-    // Tile with tokens tok0 .. tok0 + 15; those outside [lo, len) are masked
-    // (their bytes may be anything, NaN included).
-    NVFP4_DEV void tile(const uint8_t* tp, int tok0, int lo, int len) {
-        const bool edge = tok0 < lo || tok0 + kKvTile > len;
+    // kStep tiles with tokens tok0 .. tok0 + 16 kStep - 1 at tp[0], tp[1]; tokens
+    // outside [lo, hi) are masked (their bytes may be anything, NaN included).
+    static constexpr int kStep = C::kStep;
+    NVFP4_DEV void tiles(const uint8_t* const (&tp)[kStep], int tok0, int lo, int hi) {
+        const bool edge = tok0 < lo || tok0 + kStep * kKvTile > hi;
+        const int lane = threadIdx.x & 31, g = lane >> 2;
+        float s[kStep][NT][4];
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) scores(tp[u], s[u]);
+        // ---- softmax: tokens tok0 + 16 u + g (c 0, 1) and + 8 (c 2, 3), columns 2t, 2t + 1
+        uint32_t ph[kStep][NT][2], pl[kStep][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float x[kStep][4];
+#pragma unroll
+            for (int u = 0; u < kStep; ++u)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[u][c] = s[u][n][c] * f[n][c & 1];
+            if (edge) {
+#pragma unroll
+                for (int u = 0; u < kStep; ++u)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int tok = tok0 + u * kKvTile + g + 8 * (c >> 1);
+                        if (tok < lo || tok >= hi) x[u][c] = __int_as_float(0xff800000);
+                    }
+            }
+            // the running maximum is raised only when a score passes it by
+            // more than 2^8 in weight: it only guards the range (weights stay
+            // below 2^8, sums in fp32), so most tiles need no exchange
+            float up[2] = {fmaxf(x[0][0], x[0][2]), fmaxf(x[0][1], x[0][3])};
+            if constexpr (kStep == 2) {
+                up[0] = fmaxf(up[0], fmaxf(x[1][0], x[1][2]));
+                up[1] = fmaxf(up[1], fmaxf(x[1][1], x[1][3]));
+            }
+            if (__any_sync(0xffffffffu, up[0] > m[n][0] + 8.0f || up[1] > m[n][1] + 8.0f)) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float mx = up[c];
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    mx = fmaxf(mx, m[n][c]);
+                    const float al = weight(m[n][c], mx);
+                    m[n][c] = mx;
+                    l[n][c] *= al;
+#pragma unroll
+                    for (int k = 0; k < C::kMt; ++k) {
+                        o[n][k][c] *= al;
+                        o[n][k][2 + c] *= al;
+                    }
+                }
+            }
+            const float m0 = m[n][0] == __int_as_float(0xff800000) ? 0.0f : m[n][0];
+            const float m1 = m[n][1] == __int_as_float(0xff800000) ? 0.0f : m[n][1];
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) {
+                const float p[4] = {ex2(x[u][0] - m0), ex2(x[u][1] - m1), ex2(x[u][2] - m0), ex2(x[u][3] - m1)};
+                l[n][0] += p[0] + p[2];
+                l[n][1] += p[1] + p[3];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float a = p[2 * h], b = p[2 * h + 1];
+                    const uint32_t hi_part = kBf16 ? pack_b16(a, b) : pack_f16(a, b);
+                    ph[u][n][h] = movmatrix_trans(hi_part);
+                    if constexpr (kSplit) {
+                        float ra, rb;
+                        if constexpr (kBf16) {
+                            ra = a - bf16lo_to_f32(hi_part);
+                            rb = b - bf16hi_to_f32(hi_part);
+                        } else {
+                            const float2 r = f16x2_to_f32x2(hi_part);
+                            ra = a - r.x;
+                            rb = b - r.y;
+                        }
+                        pl[u][n][h] = movmatrix_trans(kBf16 ? pack_b16(ra, rb) : pack_f16(ra, rb));
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) values(tp[u], edge, tok0 + u * kKvTile, lo, hi, ph[u], pl[u]);
+    }
+
+    // S^T = K Q^T of a tile (before the factor): this thread's rows g and g + 8.
+    NVFP4_DEV void scores(const uint8_t* tp, float (&sum)[NT][4]) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const uint8_t* ks = tp + 32 * C::kDb;  // key scales, then value scales
-        // ---- S^T = K Q^T: this thread's rows g and g + 8
         float s[NT][2][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -371,21 +412,18 @@ struct Warp {
             lds<kUk>(tp + (g + 8) * C::kDb + at, w1);
             if constexpr (FMT == NVFP4_KV_NVFP4) {
                 const uint8_t* sp = ks + g * C::kSb + (off >> 3);
-                const KeyScale sc0 = key_scale(sp), sc1 = key_scale(sp + 8 * C::kSb);
+                uint32_t sc0[2], sc1[2];
+                key_scale(sp, sc0);
+                key_scale(sp + 8 * C::kSb, sc1);
 #pragma unroll
                 for (int w = 0; w < kUk / 4; ++w) {
                     uint32_t a0[4], a1[4];
-                    if (w < kBitsFrom) {
-                        e2m1x8_to_f16x2(w0[w], a0);
-                        e2m1x8_to_f16x2(w1[w], a1);
-                    } else {
-                        e2m1x8_to_f16x2_bits(w0[w], a0);
-                        e2m1x8_to_f16x2_bits(w1[w], a1);
-                    }
+                    e2m1x8_to_f16x2(w0[w], a0);
+                    e2m1x8_to_f16x2(w1[w], a1);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        a0[e] = mul_f16x2(a0[e], w < kBitsFrom ? sc0.lo0 : sc0.hi[w >> 1]);
-                        a1[e] = mul_f16x2(a1[e], w < kBitsFrom ? sc1.lo0 : sc1.hi[w >> 1]);
+                    for (int e = 0; e < 4; ++e) {  // E2M1 x E4M3: exact in fp16
+                        a0[e] = mul_f16x2(a0[e], sc0[w >> 1]);
+                        a1[e] = mul_f16x2(a1[e], sc1[w >> 1]);
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
@@ -399,9 +437,8 @@ struct Warp {
             } else if constexpr (FMT == NVFP4_KV_E4M3) {
 #pragma unroll
                 for (int w = 0; w < kUk / 4; ++w) {
-                    uint32_t a0, a1, a2, a3;
-                    e4m3x4_to_f16x2_bits(w0[w], a0, a2);
-                    e4m3x4_to_f16x2_bits(w1[w], a1, a3);
+                    const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)w0[w]), a2 = e4m3x2_to_f16x2((uint16_t)(w0[w] >> 16));
+                    const uint32_t a1 = e4m3x2_to_f16x2((uint16_t)w1[w]), a3 = e4m3x2_to_f16x2((uint16_t)(w1[w] >> 16));
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const int at_q = i * (kEk / 2) + 2 * w;
@@ -419,70 +456,17 @@ struct Warp {
                     }
             }
         }
-        // ---- softmax: tokens tok0 + g (c 0, 1) and tok0 + g + 8 (c 2, 3), columns 2t, 2t + 1
-        uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float x[4];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                x[c] = (s[n][0][c] + s[n][1][c]) * f[n][c & 1];
-            }
-            if (edge) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int tok = tok0 + g + 8 * (c >> 1);
-                    if (tok < lo || tok >= len) x[c] = __int_as_float(0xff800000);
-                }
-            }
-            // the running maximum is raised only when a score passes it by
-            // more than 2^8 in weight: it only guards the range (weights stay
-            // below 2^8, sums in fp32), so most tiles need no exchange
-            const float up0 = fmaxf(x[0], x[2]), up1 = fmaxf(x[1], x[3]);
-            if (__any_sync(0xffffffffu, up0 > m[n][0] + 8.0f || up1 > m[n][1] + 8.0f)) {
-                float mx[2] = {up0, up1};
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], d));
-                    mx[c] = fmaxf(mx[c], m[n][c]);
-                    const float al = weight(m[n][c], mx[c]);
-                    m[n][c] = mx[c];
-                    l[n][c] *= al;
-#pragma unroll
-                    for (int k = 0; k < C::kMt; ++k) {
-                        o[n][k][c] *= al;
-                        o[n][k][2 + c] *= al;
-                    }
-                }
-            }
-            float p[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float mm = m[n][c & 1];
-                p[c] = ex2(x[c] - (mm == __int_as_float(0xff800000) ? 0.0f : mm));
-            }
-            l[n][0] += p[0] + p[2];
-            l[n][1] += p[1] + p[3];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float a = p[2 * h], b = p[2 * h + 1];
-                const uint32_t hi = kBf16 ? pack_b16(a, b) : pack_f16(a, b);
-                ph[n][h] = movmatrix_trans(hi);
-                if constexpr (kSplit) {
-                    float ra, rb;
-                    if constexpr (kBf16) {
-                        ra = a - bf16lo_to_f32(hi);
-                        rb = b - bf16hi_to_f32(hi);
-                    } else {
-                        const float2 r = f16x2_to_f32x2(hi);
-                        ra = a - r.x;
-                        rb = b - r.y;
-                    }
-                    pl[n][h] = movmatrix_trans(kBf16 ? pack_b16(ra, rb) : pack_f16(ra, rb));
-                }
-            }
-        }
+            for (int c = 0; c < 4; ++c) sum[n][c] = s[n][0][c] + s[n][1][c];
+    }
+
+    // O^T += V^T P^T of a tile.
+    NVFP4_DEV void values(const uint8_t* tp, bool edge, int tok0, int lo, int len, const uint32_t (&ph)[NT][2],
+                          const uint32_t (&pl)[NT][2]) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const uint8_t* ks = tp + 32 * C::kDb;
         // ---- O^T += V^T P^T: this thread's columns of tokens 2t, 2t + 1, 2t + 8, 2t + 9
         const uint8_t* vp = tp + 16 * C::kDb;
         const uint8_t* vs = ks + 16 * C::kSb;
@@ -567,8 +551,9 @@ struct Warp {
         }
     }
 
-    // A value that depends on everything the tile read from shared memory: one
-    // accumulator of each value unit (the scores, hence all keys, feed them all).
+    // A value that depends on everything the last tiles read from shared memory:
+    // one accumulator of each value unit (the scores, hence all keys, feed them
+    // all; a step's tiles add to the accumulators in turn).
     NVFP4_DEV uint32_t depend() const {
         uint32_t d = 0;
 #pragma unroll
@@ -641,6 +626,41 @@ struct Warp {
             }
     }
 };
+
+// Waits for the next `count` (<= kStep) tiles of a warp's ring.  Of a step of
+// two with one tile left the second pointer names bytes that are masked.
+template <int S>
+struct Step {
+    bool ok;
+    uint32_t slot, second, phase;  // the slot after the step's, the step's second, the phase after it
+};
+template <int kStep, int S>
+NVFP4_DEV Step<S> wait_tiles(const uint8_t* ring, int tile, uint64_t* full, uint32_t slot, uint32_t phase,
+                             uint32_t count, int* status, const uint8_t* (&tp)[kStep]) {
+    Step<S> r;
+    bool ok = mbar_wait(&full[slot], phase, status);
+    tp[0] = ring + slot * tile;
+    uint32_t next = slot + 1, ph = phase;
+    if (next == (uint32_t)S) next = 0, ph ^= 1;
+    r.second = next;
+    if constexpr (kStep == 2) {
+        tp[1] = ring + next * tile;
+        if (count == 2) {
+            ok = mbar_wait(&full[next], ph, status) && ok;
+            if (++next == (uint32_t)S) next = 0, ph ^= 1;
+        }
+    }
+    r.slot = next;
+    r.phase = ph;
+    r.ok = __all_sync(0xffffffffu, ok);
+    return r;
+}
+// After a copy that never arrived: waits (again bounded) for every copy that may
+// still be in flight.
+template <int S>
+NVFP4_DEV void drain(uint64_t* full, uint32_t i, uint32_t n_warp, int* status) {
+    for (uint32_t k = i; k < i + S && k < n_warp; ++k) mbar_wait(&full[k % S], (k / S) & 1, status);
+}
 
 // One column of several pieces joined by a warp; a lane holds D / 32
 // consecutive elements of the head.
@@ -819,23 +839,32 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
         uint32_t begun = at.j;  // tile of the segment this piece starts with
         uint32_t slot = 0, phase = 0;
         wk.start(a, k_gs);
-        for (uint32_t i = 0; i < n_warp; ++i) {
-            const bool ok = mbar_wait(&full[slot], phase, a.status);
-            if (!__all_sync(0xffffffffu, ok)) {
-                // a copy that never arrived: wait (again bounded) for the others and stop
-                for (uint32_t k = i + 1; k < i + S && k < n_warp; ++k) mbar_wait(&full[k % S], (k / S) & 1, a.status);
+        for (uint32_t i = 0; i < n_warp;) {
+            // this step's tiles: up to kStep, of one segment
+            const uint32_t count = min((uint32_t)C::kStep, min(n_warp - i, at.tiles - at.j));
+            const uint8_t* tp[C::kStep];
+            const Step<S> step = wait_tiles<C::kStep, S>(ring, C::kTile, full, slot, phase, count, a.status, tp);
+            if (!step.ok) {
+                drain<S>(full, i, n_warp, a.status);
                 break;
             }
-            const uint8_t* tp = ring + slot * C::kTile;
-            wk.tile(tp, tok0, lo, len);
-            const uint32_t next = i + S;
-            if ((next & 31) == 0) look_up(next, at, i);
-            refill(next, slot, wk.depend());
-            tok0 += kKvTile;
-            if (++slot == (uint32_t)S) slot = 0, phase ^= 1;
+            wk.tiles(tp, tok0, lo, min(len, tok0 + (int)count * kKvTile));
+            const uint32_t dep = wk.depend();
+#pragma unroll
+            for (uint32_t u = 0; u < (uint32_t)C::kStep; ++u) {
+                if (u < count) {
+                    const uint32_t next = i + u + S;
+                    if ((next & 31) == 0) look_up(next, at, i);
+                    refill(next, u ? step.second : slot, dep);
+                }
+            }
+            slot = step.slot, phase = step.phase;
+            tok0 += (int)count * kKvTile;
+            i += count;
+            at.j += count;
             // ---- end of the segment or of the range
-            const bool ends = at.j + 1 == at.tiles;
-            if (ends || i + 1 == n_warp) {
+            const bool ends = at.j == at.tiles;
+            if (ends || i == n_warp) {
                 wk.scale_values(v_gs);
                 if (ends && begun == 0) {
                     wk.store_output(a, (int)at.b, (int)hk, (int)chunk);
@@ -848,8 +877,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
                     }
                 }
             }
-            ++at.j;
-            if (ends && i + 1 < n_warp) {  // the next segment
+            if (ends && i < n_warp) {  // the next segment
                 at.j = begun = 0;
                 if (++at.s == hc) {
                     at.s = 0;
@@ -951,18 +979,27 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
     wk.start(a, k_gs);
     uint32_t slot = 0, phase = 0;
     int tok0 = (int)j0 * kKvTile;
-    for (uint32_t i = 0; i < n_warp; ++i) {
-        const bool ok = mbar_wait(&full[slot], phase, a.status);
-        if (!__all_sync(0xffffffffu, ok)) {
-            for (uint32_t k = i + 1; k < i + S && k < n_warp; ++k) mbar_wait(&full[k % S], (k / S) & 1, a.status);
+    for (uint32_t i = 0; i < n_warp;) {
+        const uint32_t count = min((uint32_t)C::kStep, n_warp - i);
+        const uint8_t* tp[C::kStep];
+        const Step<S> step = wait_tiles<C::kStep, S>(ring, C::kTile, full, slot, phase, count, a.status, tp);
+        if (!step.ok) {
+            drain<S>(full, i, n_warp, a.status);
             break;
         }
-        wk.tile(ring + slot * C::kTile, tok0, lo, len);
-        const uint32_t next = i + S;
-        if ((next & 31) == 0) look_up(next);
-        refill(next, slot, wk.depend());
-        tok0 += kKvTile;
-        if (++slot == (uint32_t)S) slot = 0, phase ^= 1;
+        wk.tiles(tp, tok0, lo, min(len, tok0 + (int)count * kKvTile));
+        const uint32_t dep = wk.depend();
+#pragma unroll
+        for (uint32_t u = 0; u < (uint32_t)C::kStep; ++u) {
+            if (u < count) {
+                const uint32_t next = i + u + S;
+                if ((next & 31) == 0) look_up(next);
+                refill(next, u ? step.second : slot, dep);
+            }
+        }
+        slot = step.slot, phase = step.phase;
+        tok0 += (int)count * kKvTile;
+        i += count;
     }
     wk.scale_values(v_gs);
     wk.store_piece(reinterpret_cast<float*>(ring));
