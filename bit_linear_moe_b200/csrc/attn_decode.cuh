@@ -182,18 +182,23 @@ NVFP4_DEV void seen_range(const Args& a, int b, int& lo, int& len) {
     lo = (a.window > 0 && len > a.window) ? len - a.window : 0;
 }
 
-// Where tile jt of sequence b lies, for key head hk.  A page out of range is
-// reported and page 0 read in its place.
-template <int TILE>
-NVFP4_DEV const uint8_t* tile_address(const Args& a, uint32_t b, uint32_t hk, uint32_t jt) {
+// The page-table entry of tile jt of sequence b, and where that tile lies for
+// key head hk.  A page out of range is reported and page 0 read in its place.
+NVFP4_DEV uint32_t page_of(const Args& a, uint32_t jt) {
     const uint32_t per = (uint32_t)(a.c.page_size / kKvTile);
-    const uint32_t pi = (per & (per - 1)) == 0 ? jt >> (31 - __clz(per)) : jt / per;
-    int64_t page = a.table[(int64_t)b * a.table_ld + pi];
+    return (per & (per - 1)) == 0 ? jt >> (31 - __clz(per)) : jt / per;
+}
+NVFP4_DEV int32_t table_entry(const Args& a, uint32_t b, uint32_t jt) {
+    return a.table[(int64_t)b * a.table_ld + page_of(a, jt)];
+}
+template <int TILE>
+NVFP4_DEV const uint8_t* tile_in_page(const Args& a, int64_t page, uint32_t hk, uint32_t jt) {
+    const uint32_t per = (uint32_t)(a.c.page_size / kKvTile);
     if (page < 0 || page >= a.c.num_pages) {
         if (a.status) atomicExch(a.status, NVFP4_ERR_PAGE);
         page = 0;
     }
-    return a.c.data + ((page * a.c.heads + hk) * per + (jt - pi * per)) * TILE;
+    return a.c.data + ((page * a.c.heads + hk) * per + (jt - page_of(a, jt) * per)) * TILE;
 }
 
 // Writes out[v] (eight consecutive columns) of one query head.
@@ -580,9 +585,12 @@ struct Warp {
 
     // This warp's piece to `dst`.
     NVFP4_DEV void store_piece(float* dst) {
+        finish_sums();
+        write_piece(dst);
+    }
+    NVFP4_DEV void write_piece(float* dst) const {
         const int lane = threadIdx.x & 31, t = lane & 3;
         constexpr int cols = 8 * NT;
-        finish_sums();
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -601,8 +609,11 @@ struct Warp {
 
     // A whole segment, straight to the output.
     NVFP4_DEV void store_output(const Args& a, int b, int hk, int chunk) {
-        const int lane = threadIdx.x & 31, t = lane & 3;
         finish_sums();
+        write_output(a, b, hk, chunk);
+    }
+    NVFP4_DEV void write_output(const Args& a, int b, int hk, int chunk) const {
+        const int lane = threadIdx.x & 31, t = lane & 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -808,7 +819,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
                 if (p.j >= p.tiles) p = place_of(w0 + i, hc, first, B);
                 int lo, len;
                 seen_range(a, (int)p.b, lo, len);
-                addr = tile_address<C::kTile>(a, p.b, p.s / (uint32_t)a.chunks, (uint32_t)(lo / kKvTile) + p.j);
+                const uint32_t jt = (uint32_t)(lo / kKvTile) + p.j;
+                addr = tile_in_page<C::kTile>(a, table_entry(a, p.b, jt), p.s / (uint32_t)a.chunks, jt);
             }
         };
         // `dep` is made of registers that hold the results of everything read
@@ -965,7 +977,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
 
     const uint8_t* addr = nullptr;
     auto look_up = [&](uint32_t i0) {
-        if (i0 + lane < n_warp) addr = tile_address<C::kTile>(a, b, hk, j0 + i0 + lane);
+        const uint32_t jt = j0 + i0 + lane;
+        if (i0 + lane < n_warp) addr = tile_in_page<C::kTile>(a, table_entry(a, b, jt), hk, jt);
     };
     auto refill = [&](uint32_t i, uint32_t slot, uint32_t dep) {  // as in attn_decode_kernel
         if (i < n_warp && lane == (int)(i & 31)) {
@@ -1132,6 +1145,28 @@ static bool allow_smem(K kern, std::atomic<uint64_t>& done, int bytes) {
     return true;
 }
 
+// The join: a warp per row, or a CTA per row where rows may have many pieces.
+template <int D, int NT, typename YT>
+static int run_join(const Args& a, int64_t grid, cudaStream_t st) {
+    cudaLaunchAttribute attr[1];
+    set_pdl_attr(attr[0]);
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int64_t rows = (int64_t)a.B * a.q_heads;
+    cudaError_t e;
+    if ((int64_t)a.B * a.c.heads * a.chunks * 8 > grid) {
+        cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+        e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D, NT, YT, 8>, a);
+    } else {
+        cfg.gridDim = dim3((unsigned)rows);
+        e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D, NT, YT, 1>, a);
+    }
+    return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+}
+
 template <int FMT, int D, int NT, typename YT>
 static int run(const Args& a, const Shape& sh, cudaStream_t st) {
     using C = Cfg<FMT, D, NT>;
@@ -1169,19 +1204,7 @@ static int run(const Args& a, const Shape& sh, cudaStream_t st) {
     cfg.gridDim = dim3((unsigned)sh.grid);
     cfg.dynamicSmemBytes = (size_t)C::kFixed + (size_t)((a.B + 4) / 4 * 4) * 4 + 16;
     if (cudaLaunchKernelEx(&cfg, attn_decode_kernel<FMT, D, NT, YT>, a) != cudaSuccess) return NVFP4_ERR_LAUNCH;
-    // the join: a warp per row, or a CTA per row where rows may have many pieces
-    const int64_t rows = (int64_t)a.B * a.q_heads;
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = 0;
-    cudaError_t e;
-    if (segments * 8 > sh.grid) {
-        cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
-        e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D, NT, YT, 8>, a);
-    } else {
-        cfg.gridDim = dim3((unsigned)rows);
-        e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D, NT, YT, 1>, a);
-    }
-    return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
+    return run_join<D, NT, YT>(a, sh.grid, st);
 }
 
 // Query columns per pass: 16 where the key head has more than 8 query heads

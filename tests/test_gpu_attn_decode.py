@@ -16,6 +16,10 @@ from oracle.stack import bf16_round
 pytestmark = pytest.mark.gpu
 
 FMTS = (oat.BF16, oat.E4M3, oat.NVFP4)
+# The host knows lengths only by the table's width: a narrow table is served by a cluster
+# of CTAs per (sequence, key head), a wide one by an even split of all tiles.
+WIDE = 600
+WIDTHS = pytest.mark.parametrize("extra", [0, WIDE], ids=["narrow", "wide"])
 
 
 class Batch:
@@ -92,10 +96,6 @@ class Batch:
 
 
 LENS = (0, 1, 2, 15, 16, 17, 31, 48, 100, 129)
-# The host knows lengths only by the table's width: a narrow table is served by a cluster
-# of CTAs per (sequence, key head), a wide one by an even split of all tiles.
-WIDE = 600
-WIDTHS = pytest.mark.parametrize("extra", [0, WIDE], ids=["narrow", "wide"])
 
 
 @WIDTHS
@@ -125,18 +125,19 @@ def test_window(cuda_device, fmt, D, page, window, extra):
     b.check(*b.run(window=window), window=window)
 
 
+@pytest.mark.parametrize("y_dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("D,Hkv,G,lens", [
     (128, 1, 8, (9001,)), (128, 2, 2, (4097, 33)), (64, 1, 16, (20000,)), (256, 1, 3, (6000, 0, 700)),
     (128, 4, 2, tuple(int(x) for x in np.random.default_rng(2).integers(0, 700, 60)))])
 @WIDTHS
-def test_work_split_over_ctas(cuda_device, fmt, D, Hkv, G, lens, extra):
+def test_work_split_over_ctas(cuda_device, fmt, D, Hkv, G, lens, extra, y_dtype):
     """Long sequences over many CTAs, and ragged batches whose segments end anywhere in a
     CTA's or a warp's range; fp32 output shows a join that lost or doubled a piece."""
     b = Batch(fmt, D, Hkv, G, 64, lens, extra_cols=extra)
-    y, lse = b.run(y_dtype=torch.float32)
+    y, lse = b.run(y_dtype=y_dtype)
     b.check(y, lse)
-    y2, lse2 = b.run(y_dtype=torch.float32)
+    y2, lse2 = b.run(y_dtype=y_dtype)
     assert torch.equal(y, y2) and torch.equal(lse, lse2)         # the same bits
 
 
