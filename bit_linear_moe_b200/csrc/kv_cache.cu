@@ -18,8 +18,11 @@
 // the same inputs give the same bits in the separate and the fused kernel.
 //
 // All three kernels move each byte once and are bound by HBM for long chunks
-// and by latency for decode steps; a thread owns a unit of 16 elements (one
-// NVFP4 block).  All are programmatic dependents.
+// and by latency for decode steps.  A thread takes units of 16 elements (one
+// NVFP4 block) of a row, a row being one head of one token.  A warp takes one
+// head at a time and the CTA's tokens along it, its lanes covering 2 to 8 whole
+// rows, so that everything but a row's place is known per head; the loads of
+// four rows per lane go out together.  All are programmatic dependents.
 #include "internal.h"
 #include "kv_layout.cuh"
 #include "quotient.cuh"
@@ -66,26 +69,33 @@ struct RopeParams {
     int inverse;
 };
 
-// (cos, sin) of the CTA's tokens into cs[token][pair].
+// (cos, sin) of the CTA's tokens, ordered so that neighbouring lanes read
+// neighbouring words: pair p of token tl at [tl][p % w][p / w], w the pairs of a
+// run of 8 elements (8 where a run holds one element of each pair, else 4).
 NVFP4_DEV void rope_angles(const RopeParams& rp, int64_t t0, int nt, float2* cs) {
+    const int lw = rp.layout == NVFP4_ROPE_HALF ? 3 : 2, runs = rp.pairs >> lw;
     for (int i = threadIdx.x; i < nt * rp.pairs; i += blockDim.x) {
         const int tl = i / rp.pairs, p = i - tl * rp.pairs;
         const double turns = (double)rp.positions[t0 + tl] * rp.freqs[p];
         double s, c;
         sincospi(2.0 * (turns - rint(turns)), &s, &c);
         if (rp.inverse) s = -s;
-        cs[i] = make_float2((float)(c * rp.mscale), (float)(s * rp.mscale));
+        cs[tl * rp.pairs + (p & ((1 << lw) - 1)) * runs + (p >> lw)] =
+            make_float2((float)(c * rp.mscale), (float)(s * rp.mscale));
     }
 }
 
-// Unit j of a head: the element offsets of its two runs of 8.
-NVFP4_DEV void rope_runs(const RopeParams& rp, int j, int& lo, int& hi) {
-    if (j * 8 < rp.pairs && rp.layout == NVFP4_ROPE_HALF) {
+// Unit j of a head: the element offsets of its two runs of 8.  Both runs of a
+// region (the rotated elements, the rest) advance by 8 per unit, so that a
+// warp's 16-byte accesses are contiguous in either layout.
+NVFP4_DEV void rope_runs(const RopeParams& rp, int j, int D, int& lo, int& hi) {
+    const int n8 = rp.pairs >> 3;
+    if (j < n8) {
         lo = j * 8;
         hi = rp.pairs + j * 8;
     } else {
-        lo = j * 16;
-        hi = lo + 8;
+        lo = 2 * rp.pairs + (j - n8) * 8;
+        hi = lo + (D >> 1) - rp.pairs;
     }
 }
 
@@ -95,28 +105,70 @@ NVFP4_DEV void rotate(float& a, float& b, float2 cs) {
     b = __fadd_rn(__fmul_rn(y, cs.x), __fmul_rn(x, cs.y));
 }
 
-// Rotates the two runs of unit j (cs: the token's angles).
-NVFP4_DEV void rope_unit(const RopeParams& rp, int j, const float2* cs, float (&lo)[8], float (&hi)[8]) {
-    if (j * 8 >= rp.pairs) return;
-    cs += j * 8;
+// Rotates the two runs of unit j of token tl.
+NVFP4_DEV void rope_unit(const RopeParams& rp, int j, int tl, const float2* cs, float (&lo)[8], float (&hi)[8]) {
+    const int n8 = rp.pairs >> 3;
+    if (j >= n8) return;
+    cs += tl * rp.pairs + j;
     if (rp.layout == NVFP4_ROPE_HALF) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) rotate(lo[i], hi[i], cs[i]);
+        for (int i = 0; i < 8; ++i) rotate(lo[i], hi[i], cs[i * n8]);
     } else {
+        const int runs = 2 * n8;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            rotate(lo[2 * i], lo[2 * i + 1], cs[i]);
-            rotate(hi[2 * i], hi[2 * i + 1], cs[4 + i]);
+            rotate(lo[2 * i], lo[2 * i + 1], cs[i * runs]);
+            rotate(hi[2 * i], hi[2 * i + 1], cs[i * runs + n8]);
         }
     }
 }
 
-constexpr int kCtaThreads = 256;
+constexpr int kCtaThreads = 256, kWarps = kCtaThreads / 32;
+constexpr int kBatch = 2;       // rows per lane whose loads go out together (reads of the cache: twice that)
+constexpr int kPasses = 4;      // rows per lane and head in a full CTA
+constexpr int kMaxTokens = 32;  // tokens per CTA, at most
 
-// A CTA takes `tt` tokens and `hc` heads; consecutive threads take
-// consecutive units of a head, so a warp's loads are contiguous.
+// Units are as raw 16-byte words while they are on their way.
+template <typename T>
+struct Raw16 {
+    uint4 w[sizeof(T)];  // 16 elements: 2 words of bf16, 4 of fp32
+    // elements 0 .. 7 from lo, 8 .. 15 from hi
+    NVFP4_DEV void load(const T* lo, const T* hi) {
+        constexpr int h = sizeof(T) / 2;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            w[i] = reinterpret_cast<const uint4*>(lo)[i];
+            w[h + i] = reinterpret_cast<const uint4*>(hi)[i];
+        }
+    }
+    NVFP4_DEV void clear() {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T); ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    NVFP4_DEV void values(float (&lo)[8], float (&hi)[8]) const {
+        constexpr int h = sizeof(T) / 2;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            lo[i] = at(0, i);
+            hi[i] = at(h, i);
+        }
+    }
+
+   private:
+    NVFP4_DEV float at(int base, int i) const {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t x = word(w[base], i >> 1);
+            return (i & 1) ? bf16hi_to_f32(x) : bf16lo_to_f32(x);
+        } else {
+            return __uint_as_float(word(w[base + (i >> 2)], i & 3));
+        }
+    }
+    static NVFP4_DEV uint32_t word(const uint4& v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; }
+};
+
+// A CTA takes `tt` tokens and `hc` heads.
 template <typename XT, typename YT>
-__global__ void __launch_bounds__(kCtaThreads) rope_kernel(const XT* x, int64_t T, int heads, int units, int64_t x_ld,
+__global__ void __launch_bounds__(kCtaThreads, 4) rope_kernel(const XT* x, int64_t T, int heads, int units, int64_t x_ld,
                                                            RopeParams rp, YT* y, int64_t y_ld, int tt, int hc) {
     extern __shared__ __align__(16) uint8_t smem[];
     float2* cs = reinterpret_cast<float2*>(smem);
@@ -124,24 +176,46 @@ __global__ void __launch_bounds__(kCtaThreads) rope_kernel(const XT* x, int64_t 
     griddep_wait();
     const int64_t t0 = (int64_t)blockIdx.x * tt;
     const int nt = (int)(T - t0 < tt ? T - t0 : tt);
-    const int h0 = blockIdx.y * hc, nh = min(heads - h0, hc);
+    const int h0 = blockIdx.y * hc, h1 = min(heads, h0 + hc);
+    // lanes: `per` rows of `units` units (one row, 32 units at a time, for wide heads)
+    const int lane = threadIdx.x & 31, per = units < 32 ? 32 / units : 1;
+    const int row = units < 32 ? lane / units : 0, D = units * 16;
+    const int first = row < per ? row : kMaxTokens;  // lanes past the last row idle
+    int j = lane - row * units, h = h0 + (threadIdx.x >> 5), tl0 = first, lo, hi;
+    rope_runs(rp, j, D, lo, hi);
+    Raw16<XT> raw[kBatch];
+    auto load = [&]() {
+        const XT* xp = x + (t0 + tl0) * x_ld + h * D;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (h < h1 && tl0 + k * per < nt) raw[k].load(xp + k * per * x_ld + lo, xp + k * per * x_ld + hi);
+    };
+    load();  // on their way while the angles are found
     rope_angles(rp, t0, nt, cs);
     __syncthreads();
-    const int per = nh * units;
-    for (int u = threadIdx.x; u < nt * per; u += kCtaThreads) {
-        const int tl = u / per, hj = u - tl * per;
-        const int h = h0 + hj / units, j = hj % units;
-        int lo, hi;
-        rope_runs(rp, j, lo, hi);
-        const int64_t col = (int64_t)h * units * 16;
-        const XT* xp = x + (t0 + tl) * x_ld + col;
-        float a[8], b[8];
-        load8(xp + lo, a);
-        load8(xp + hi, b);
-        rope_unit(rp, j, cs + tl * rp.pairs, a, b);
-        YT* yp = y + (t0 + tl) * y_ld + col;
-        store8(yp + lo, a);
-        store8(yp + hi, b);
+    while (h < h1) {
+        YT* yp = y + (t0 + tl0) * y_ld + h * D;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (tl0 + k * per < nt) {
+                float a[8], b[8];
+                raw[k].values(a, b);
+                rope_unit(rp, j, tl0 + k * per, cs, a, b);
+                store8(yp + k * per * y_ld + lo, a);
+                store8(yp + k * per * y_ld + hi, b);
+            }
+        }
+        tl0 += kBatch * per;
+        if (tl0 >= nt) {
+            tl0 = first;
+            j += 32;
+            if (j >= units) {
+                j = lane - row * units;
+                h += kWarps;
+            }
+            rope_runs(rp, j, D, lo, hi);
+        }
+        load();
     }
 }
 
@@ -176,37 +250,91 @@ NVFP4_DEV uint32_t e4m3x2_of_quotients(float a, float b, const GsPar& g) {
     return f32x2_to_e4m3(__fdiv_rn(a, g.gs), __fdiv_rn(b, g.gs));
 }
 
-// Block j (16 elements) of tile row r, into the keys (which 0) or values (1)
-// of the tile.
-template <int FMT>
-NVFP4_DEV void store_block(uint8_t* tile, int which, int r, int j, int D, const float (&v)[16], const GsPar& g) {
-    const int db = kv_code_bytes(FMT, D), pieces = db >> 4;
-    uint8_t* row = tile + (which * kKvTile + r) * db;
-    if constexpr (FMT == NVFP4_KV_BF16) {
+// Where a token's rows lie: bytes from a head's first tile to its tile's codes
+// (key rows; -1: not stored), the tile row, and how its pieces are turned.
+struct Slot {
+    int64_t tile;
+    int r, turn;
+};
+template <int FMT, int D>
+NVFP4_DEV void find_slots(const KvView& c, const int64_t* slots, int64_t t0, int nt, int64_t head_bytes, int* status,
+                          Slot* out) {
+    if ((int)threadIdx.x >= nt) return;
+    const int64_t slot = slots[t0 + threadIdx.x];
+    Slot s{-1, 0, 0};
+    if (slot >= 0) {
+        // (a 32-bit division where it does, which is nearly always)
+        const int64_t page = slot >> 31 ? slot / c.page_size : (int64_t)((uint32_t)slot / (uint32_t)c.page_size);
+        const int in = (int)(slot - page * c.page_size);
+        s.r = in % kKvTile;
+        s.turn = kv_turn(s.r, kv_code_bytes(FMT, D) / 16);
+        if (page < c.num_pages)
+            s.tile = page * c.heads * head_bytes + (int64_t)(in / kKvTile) * kv_tile_bytes(FMT, D);
+        else if (status)
+            atomicExch(status, NVFP4_ERR_PAGE);
+    }
+    out[threadIdx.x] = s;
+}
+
+// Address of byte o of row s.r of the keys (which 0) or values (1) of a tile.
+template <int FMT, int D>
+NVFP4_DEV uint8_t* row_at(uint8_t* tile, int which, const Slot& s, int o) {
+    return tile + (which * kKvTile + s.r) * kv_code_bytes(FMT, D) + ((((o >> 4) ^ s.turn) << 4) | (o & 15));
+}
+template <int D>
+NVFP4_DEV uint8_t* scale_at(uint8_t* tile, int which, const Slot& s, int j) {
+    return tile + 2 * kKvTile * kv_code_bytes(NVFP4_KV_NVFP4, D) + (which * kKvTile + s.r) * (D / 16) + j;
+}
+
+// E2M1 codes (a word) of v[j] / r, j < 8: e2m1x16_of_quotients' argument for
+// half a block (amax: the block's).
+NVFP4_DEV uint32_t e2m1x8_of_quotients(const float (&v)[8], float amax, float r) {
+    const float inv = rcp_safe(r) ? rcp_approx(r) : 0.0f;
+    uint32_t code = 0u, diff = 0xFFFFFFFFu;
+    if (inv != 0.0f && __fmul_rn(amax, inv) < 15.0f) {
+        float lo[8], hi[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = v[8 * h + i];
-            *reinterpret_cast<uint4*>(row + kv_place(r, (2 * j + h) * 16, pieces)) = pack8_bf16(w);
+        for (int j = 0; j < 8; ++j) {
+            const float p = __fmul_rn(v[j], inv);
+            lo[j] = __fmul_rn(p, kBracketLo);
+            hi[j] = __fmul_rn(p, kBracketHi);
         }
-    } else if constexpr (FMT == NVFP4_KV_E4M3) {
-        uint32_t w[4];
+        code = f32x8_to_e2m1(hi);
+        diff = f32x8_to_e2m1(lo) ^ code;
+    }
+    if (diff) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = e4m3x2_of_quotients(v[4 * i], v[4 * i + 1], g) |
-                   (e4m3x2_of_quotients(v[4 * i + 2], v[4 * i + 3], g) << 16);
-        *reinterpret_cast<uint4*>(row + kv_place(r, j * 16, pieces)) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int j = 0; j < 8; ++j)
+            if (diff & (0xFu << (4 * j))) code = (code & ~(0xFu << (4 * j))) | (e2m1_of_division(v[j], r) << (4 * j));
+    }
+    return code;
+}
+
+// Eight elements e .. e + 7 of a row.  NVFP4: lanes 2 i and 2 i + 1 hold the
+// halves of a block; every lane of the warp calls (live: something is stored).
+template <int FMT, int D>
+NVFP4_DEV void store_run(bool live, uint8_t* tile, int which, const Slot& s, int e, const float (&v)[8],
+                         const GsPar& g) {
+    if constexpr (FMT == NVFP4_KV_BF16) {
+        if (live) *reinterpret_cast<uint4*>(row_at<FMT, D>(tile, which, s, 2 * e)) = pack8_bf16(v);
+    } else if constexpr (FMT == NVFP4_KV_E4M3) {
+        if (live) {
+            const uint32_t w0 = e4m3x2_of_quotients(v[0], v[1], g) | (e4m3x2_of_quotients(v[2], v[3], g) << 16);
+            const uint32_t w1 = e4m3x2_of_quotients(v[4], v[5], g) | (e4m3x2_of_quotients(v[6], v[7], g) << 16);
+            *reinterpret_cast<uint2*>(row_at<FMT, D>(tile, which, s, e)) = make_uint2(w0, w1);
+        }
     } else {
         float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
-        const uint32_t sb = e4m3_of_quotient(amax, g.denom, g.inv_denom);
-        const float rsc = __fmul_rn(e4m3_to_f32(sb), g.gs);
-        uint2 packed = make_uint2(0u, 0u);
-        if (rsc != 0.0f) packed = e2m1x16_of_quotients(v, amax, rsc, rcp_safe(rsc) ? rcp_approx(rsc) : 0.0f);
-        *reinterpret_cast<uint2*>(row + kv_place(r, j * 8, pieces)) = packed;
-        tile[2 * kKvTile * db + (which * kKvTile + r) * (D >> 4) + j] = (uint8_t)sb;
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        if (live) {
+            const uint32_t sb = e4m3_of_quotient(amax, g.denom, g.inv_denom);
+            const float rsc = __fmul_rn(e4m3_to_f32(sb), g.gs);
+            *reinterpret_cast<uint32_t*>(row_at<FMT, D>(tile, which, s, e / 2)) =
+                rsc != 0.0f ? e2m1x8_of_quotients(v, amax, rsc) : 0u;
+            if ((e & 8) == 0) *scale_at<D>(tile, which, s, e / 16) = (uint8_t)sb;
+        }
     }
 }
 
@@ -225,148 +353,164 @@ struct KvWriteArgs {
     int* status;
 };
 
-constexpr int kMaxTokens = 16;  // tokens per CTA, at most
-
 // Heads 0 .. q_heads - 1 are the queries, then the keys, then the values.
-// Rotated keys pass through shared memory (bf16): a unit's two runs of 8 lie
-// in two blocks when pairs are half a head apart.
-template <typename XT, int FMT, bool ROPE>
-__global__ void __launch_bounds__(kCtaThreads) kv_write_kernel(const KvWriteArgs a) {
+// Rotated keys of the NVFP4 cache pass through the warp's own piece of shared
+// memory (bf16): a unit's two runs of 8 lie in two blocks.
+template <typename XT, int FMT, int D, bool ROPE>
+__global__ void __launch_bounds__(kCtaThreads, sizeof(XT) == 2 ? 4 : 3) kv_write_kernel(const KvWriteArgs a) {
+    constexpr int units = D / 16, per = 32 / units;
+    constexpr int batch = kBatch;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int64_t s_tile[kMaxTokens];  // byte offset of the token's tile, head 0; -1: not stored
-    __shared__ int s_row[kMaxTokens];
+    __shared__ Slot s_slot[kMaxTokens];
     griddep_launch_dependents();
     griddep_wait();
-    const int D = a.c.head_dim, units = D >> 4;
     const int64_t t0 = (int64_t)blockIdx.x * a.tt;
     const int nt = (int)(a.T - t0 < a.tt ? a.T - t0 : a.tt);
-    const int heads = a.q_heads + 2 * a.c.heads;
-    const int h0 = blockIdx.y * a.hc, nh = min(heads - h0, a.hc);
-    const int tiles = a.c.page_size / kKvTile;
-    const int64_t head_bytes = (int64_t)tiles * kv_tile_bytes(FMT, D);
-    if ((int)threadIdx.x < nt) {
-        const int64_t slot = a.slots[t0 + threadIdx.x];
-        int64_t off = -1;
-        int r = 0;
-        if (slot >= 0) {
-            const int64_t page = slot / a.c.page_size;
-            const int in = (int)(slot - page * a.c.page_size);
-            r = in % kKvTile;
-            if (page < a.c.num_pages)
-                off = page * a.c.heads * head_bytes + (int64_t)(in / kKvTile) * kv_tile_bytes(FMT, D);
-            else if (a.status)
-                atomicExch(a.status, NVFP4_ERR_PAGE);
-        }
-        s_tile[threadIdx.x] = off;
-        s_row[threadIdx.x] = r;
-    }
+    const int k0 = a.q_heads, v0 = a.q_heads + a.c.heads, heads = v0 + a.c.heads;
+    const int h0 = blockIdx.y * a.hc, h1 = min(heads, h0 + a.hc);
+    const int64_t head_bytes = (int64_t)(a.c.page_size / kKvTile) * kv_tile_bytes(FMT, D);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % units, first = lane / units;
+    int h = h0 + warp, tb = 0;
+    Raw16<XT> raw[batch];
+    auto head_of = [&](int hh) { return hh < k0 ? hh : hh >= v0 ? hh - v0 : hh - k0; };
+    auto load = [&]() {  // the lane's rows of head h from token tb on
+        if (h >= h1) return;
+        const bool is_q = h < k0, is_v = h >= v0;  // without ROPE there are no queries
+        const int64_t ld = is_q ? a.q_ld : is_v ? a.v_ld : a.k_ld;
+        const XT* src = (is_q ? (const XT*)a.q : is_v ? (const XT*)a.v : (const XT*)a.k) + (t0 + tb + first) * ld +
+                        head_of(h) * D;
+        int lo = 8 * j, hi = D / 2 + 8 * j;
+        if (ROPE && !is_v) rope_runs(a.rp, j, D, lo, hi);
+#pragma unroll
+        for (int k = 0; k < batch; ++k)
+            if (tb + first + k * per < nt) raw[k].load(src + k * per * ld + lo, src + k * per * ld + hi);
+    };
+#pragma unroll
+    for (int k = 0; k < batch; ++k) raw[k].clear();
+    load();  // on their way while slots and angles are found
+    find_slots<FMT, D>(a.c, a.slots, t0, nt, head_bytes, a.status, s_slot);
     float2* cs = reinterpret_cast<float2*>(smem);
-    __nv_bfloat16* staged = reinterpret_cast<__nv_bfloat16*>(smem + (ROPE ? a.tt * a.rp.pairs * (int)sizeof(float2) : 0));
     if constexpr (ROPE) rope_angles(a.rp, t0, nt, cs);
     GsPar gk{}, gv{};
     if constexpr (FMT != NVFP4_KV_BF16) {
         gk = gs_par(a.c.k_gs);
         gv = gs_par(a.c.v_gs);
     }
+    __nv_bfloat16* staged =
+        reinterpret_cast<__nv_bfloat16*>(smem + (ROPE ? a.tt * a.rp.pairs * (int)sizeof(float2) : 0)) +
+        warp * batch * per * D;
     __syncthreads();
-    const int k0 = a.q_heads, v0 = a.q_heads + a.c.heads;
-    const int kfirst = max(h0, k0), nk = max(0, min(h0 + nh, v0) - kfirst);  // key heads of this CTA
-    const int per = nh * units;
-    for (int u = threadIdx.x; u < nt * per; u += kCtaThreads) {
-        const int tl = u / per, hj = u - tl * per;
-        const int h = h0 + hj / units, j = hj % units;
-        const int64_t t = t0 + tl;
-        if (ROPE && h < v0) {
-            const bool is_q = h < k0;
-            if (!is_q && s_tile[tl] < 0) continue;
-            const XT* xp = is_q ? (const XT*)a.q + t * a.q_ld + (int64_t)h * D
-                                : (const XT*)a.k + t * a.k_ld + (int64_t)(h - k0) * D;
-            int lo, hi;
-            rope_runs(a.rp, j, lo, hi);
+    while (h < h1) {
+        uint8_t* base = a.c.data + head_of(h) * head_bytes;
+        const bool is_q = h < k0, is_v = h >= v0, turned = ROPE && !is_v;
+#pragma unroll
+        for (int k = 0; k < batch; ++k) {
+            const int tl = tb + first + k * per;
+            const bool in = tl < nt;
+            const Slot s = s_slot[in ? tl : 0];
+            const bool live = in && s.tile >= 0;
             float x[8], y[8];
-            load8(xp + lo, x);
-            load8(xp + hi, y);
-            rope_unit(a.rp, j, cs + tl * a.rp.pairs, x, y);
-            __nv_bfloat16* yp =
-                is_q ? a.q_out + (t * a.q_heads + h) * D : staged + (tl * nk + (h - kfirst)) * D;
-            store8(yp + lo, x);
-            store8(yp + hi, y);
-        } else {
-            if (s_tile[tl] < 0) continue;
-            const bool is_v = h >= v0;
-            const int hk = is_v ? h - v0 : h - k0;
-            const XT* xp = is_v ? (const XT*)a.v + t * a.v_ld : (const XT*)a.k + t * a.k_ld;
-            xp += (int64_t)hk * D + j * 16;
-            float x[8], y[8], w[16];
-            load8(xp, x);
-            load8(xp + 8, y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                w[i] = x[i];
-                w[8 + i] = y[i];
+            raw[k].values(x, y);
+            if (ROPE && turned) {
+                int lo, hi;
+                rope_runs(a.rp, j, D, lo, hi);
+                if (in) rope_unit(a.rp, j, tl, cs, x, y);
+                if (is_q) {
+                    if (in) {
+                        __nv_bfloat16* yp = a.q_out + ((t0 + tl) * a.q_heads + h) * D;
+                        store8(yp + lo, x);
+                        store8(yp + hi, y);
+                    }
+                } else if constexpr (FMT == NVFP4_KV_NVFP4) {
+                    store8(staged + (first + k * per) * D + lo, x);
+                    store8(staged + (first + k * per) * D + hi, y);
+                } else {  // quantized from the bf16 values
+                    const uint4 xw = pack8_bf16(x), yw = pack8_bf16(y);
+                    load8(reinterpret_cast<const __nv_bfloat16*>(&xw), x);
+                    load8(reinterpret_cast<const __nv_bfloat16*>(&yw), y);
+                    store_run<FMT, D>(live, base + s.tile, 0, s, lo, x, gk);
+                    store_run<FMT, D>(live, base + s.tile, 0, s, hi, y, gk);
+                }
+            } else {
+                store_run<FMT, D>(live, base + s.tile, is_v, s, 8 * j, x, is_v ? gv : gk);
+                store_run<FMT, D>(live, base + s.tile, is_v, s, D / 2 + 8 * j, y, is_v ? gv : gk);
             }
-            store_block<FMT>(a.c.data + s_tile[tl] + hk * head_bytes, is_v, s_row[tl], j, D, w, is_v ? gv : gk);
         }
-    }
-    if constexpr (ROPE) {
-        __syncthreads();
-        const int kper = nk * units;
-        for (int u = threadIdx.x; u < nt * kper; u += kCtaThreads) {
-            const int tl = u / kper, hj = u - tl * kper;
-            const int hl = hj / units, j = hj % units;
-            if (s_tile[tl] < 0) continue;
-            const __nv_bfloat16* xp = staged + (tl * nk + hl) * D + j * 16;
-            float x[8], y[8], w[16];
-            load8(xp, x);
-            load8(xp + 8, y);
+        if constexpr (ROPE && FMT == NVFP4_KV_NVFP4) {
+            if (!is_q && !is_v) {
+                __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                w[i] = x[i];
-                w[8 + i] = y[i];
+                for (int k = 0; k < batch; ++k) {
+                    const int tl = tb + first + k * per;
+                    const Slot s = s_slot[tl < nt ? tl : 0];
+                    const bool live = tl < nt && s.tile >= 0;
+                    float x[8], y[8];
+                    load8(staged + (first + k * per) * D + 8 * j, x);
+                    load8(staged + (first + k * per) * D + D / 2 + 8 * j, y);
+                    store_run<FMT, D>(live, base + s.tile, 0, s, 8 * j, x, gk);
+                    store_run<FMT, D>(live, base + s.tile, 0, s, D / 2 + 8 * j, y, gk);
+                }
+                __syncwarp();
             }
-            store_block<FMT>(a.c.data + s_tile[tl] + (kfirst - k0 + hl) * head_bytes, 0, s_row[tl], j, D, w, gk);
         }
+        tb += batch * per;
+        if (tb >= nt) {
+            tb = 0;
+            h += kWarps;
+        }
+        load();
     }
 }
 
 // ---- cache reads -------------------------------------------------------------
 
-// Block j of tile row r as fp32 values.
+// Eight elements e .. e + 7 of a tile row as stored, and their fp32 values.
 template <int FMT>
-NVFP4_DEV void load_block(const uint8_t* tile, int which, int r, int j, int D, float gs, float (&v)[16]) {
-    const int db = kv_code_bytes(FMT, D), pieces = db >> 4;
-    const uint8_t* row = tile + (which * kKvTile + r) * db;
+struct RawRun {
+    uint32_t c[FMT == NVFP4_KV_BF16 ? 4 : FMT == NVFP4_KV_E4M3 ? 2 : 1];
+    uint32_t sb;
+};
+template <int FMT, int D>
+NVFP4_DEV void load_run(const uint8_t* tile_, int which, const Slot& s, int e, RawRun<FMT>& x) {
+    uint8_t* tile = const_cast<uint8_t*>(tile_);
+    if constexpr (FMT == NVFP4_KV_BF16) {
+        const uint4 c = *reinterpret_cast<const uint4*>(row_at<FMT, D>(tile, which, s, 2 * e));
+        x.c[0] = c.x, x.c[1] = c.y, x.c[2] = c.z, x.c[3] = c.w;
+    } else if constexpr (FMT == NVFP4_KV_E4M3) {
+        const uint2 c = *reinterpret_cast<const uint2*>(row_at<FMT, D>(tile, which, s, e));
+        x.c[0] = c.x, x.c[1] = c.y;
+    } else {
+        x.c[0] = *reinterpret_cast<const uint32_t*>(row_at<FMT, D>(tile, which, s, e / 2));
+        x.sb = *scale_at<D>(tile, which, s, e / 16);
+    }
+}
+template <int FMT>
+NVFP4_DEV void run_values(const RawRun<FMT>& x, float gs, float (&v)[8]) {
     if constexpr (FMT == NVFP4_KV_BF16) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float w[8];
-            load8(reinterpret_cast<const __nv_bfloat16*>(row + kv_place(r, (2 * j + h) * 16, pieces)), w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[8 * h + i] = w[i];
-        }
-    } else if constexpr (FMT == NVFP4_KV_E4M3) {
-        const uint4 c = *reinterpret_cast<const uint4*>(row + kv_place(r, j * 16, pieces));
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
-            v[2 * i] = __fmul_rn(f.x, gs);
-            v[2 * i + 1] = __fmul_rn(f.y, gs);
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = bf16lo_to_f32(x.c[i]);
+            v[2 * i + 1] = bf16hi_to_f32(x.c[i]);
         }
     } else {
-        const uint2 c = *reinterpret_cast<const uint2*>(row + kv_place(r, j * 8, pieces));
-        const float s = e4m3_to_f32(tile[2 * kKvTile * db + (which * kKvTile + r) * (D >> 4) + j]);
-        const uint32_t w[2] = {c.x, c.y};
+        uint32_t p[4];
+        if constexpr (FMT == NVFP4_KV_E4M3) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t p[4];
-            e2m1x8_to_f16x2(w[h], p);
+            for (int i = 0; i < 4; ++i) p[i] = e4m3x2_to_f16x2((uint16_t)(x.c[i >> 1] >> (16 * (i & 1))));
+        } else {
+            const __half2 s = __half2half2(__ushort_as_half((unsigned short)e4m3x2_to_f16x2((uint16_t)x.sb)));
+            e2m1x8_to_f16x2(x.c[0], p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 f = f16x2_to_f32x2(p[i]);
-                v[8 * h + 2 * i] = __fmul_rn(__fmul_rn(f.x, s), gs);  // E2M1 * E4M3 is exact
-                v[8 * h + 2 * i + 1] = __fmul_rn(__fmul_rn(f.y, s), gs);
+                const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&p[i]), s);  // E2M1 * E4M3: exact
+                p[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = f16x2_to_f32x2(p[i]);
+            v[2 * i] = __fmul_rn(f.x, gs);
+            v[2 * i + 1] = __fmul_rn(f.y, gs);
         }
     }
 }
@@ -382,81 +526,73 @@ struct KvReadArgs {
 };
 
 // Heads 0 .. heads - 1 are the keys, then the values.
-template <typename YT, int FMT>
-__global__ void __launch_bounds__(kCtaThreads) kv_read_kernel(const KvReadArgs a) {
-    __shared__ int64_t s_tile[kMaxTokens];
-    __shared__ int s_row[kMaxTokens];
+template <typename YT, int FMT, int D>
+__global__ void __launch_bounds__(kCtaThreads, 4) kv_read_kernel(const KvReadArgs a) {
+    constexpr int units = D / 16, per = 32 / units;
+    __shared__ Slot s_slot[kMaxTokens];
     griddep_launch_dependents();
     griddep_wait();
-    const int D = a.c.head_dim, units = D >> 4;
     const int64_t t0 = (int64_t)blockIdx.x * a.tt;
     const int nt = (int)(a.T - t0 < a.tt ? a.T - t0 : a.tt);
-    const int h0 = blockIdx.y * a.hc, nh = min(2 * a.c.heads - h0, a.hc);
-    const int tiles = a.c.page_size / kKvTile;
-    const int64_t head_bytes = (int64_t)tiles * kv_tile_bytes(FMT, D);
-    if ((int)threadIdx.x < nt) {
-        const int64_t slot = a.slots[t0 + threadIdx.x];
-        int64_t off = -1;
-        int r = 0;
-        if (slot >= 0) {
-            const int64_t page = slot / a.c.page_size;
-            const int in = (int)(slot - page * a.c.page_size);
-            r = in % kKvTile;
-            if (page < a.c.num_pages)
-                off = page * a.c.heads * head_bytes + (int64_t)(in / kKvTile) * kv_tile_bytes(FMT, D);
-            else if (a.status)
-                atomicExch(a.status, NVFP4_ERR_PAGE);
-        }
-        s_tile[threadIdx.x] = off;
-        s_row[threadIdx.x] = r;
-    }
+    const int h0 = blockIdx.y * a.hc, h1 = min(2 * a.c.heads, h0 + a.hc);
+    const int64_t head_bytes = (int64_t)(a.c.page_size / kKvTile) * kv_tile_bytes(FMT, D);
+    find_slots<FMT, D>(a.c, a.slots, t0, nt, head_bytes, a.status, s_slot);
     float gk = 1.0f, gv = 1.0f;
     if constexpr (FMT != NVFP4_KV_BF16) {
         gk = *a.c.k_gs;
         gv = *a.c.v_gs;
     }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % units, first = lane / units;
+    const int64_t y_ld = (int64_t)a.c.heads * D;
     __syncthreads();
-    const int per = nh * units;
-    for (int u = threadIdx.x; u < nt * per; u += kCtaThreads) {
-        const int tl = u / per, hj = u - tl * per;
-        const int h = h0 + hj / units, j = hj % units;
+    for (int h = h0 + warp; h < h1; h += kWarps) {
         const bool is_v = h >= a.c.heads;
         const int hk = is_v ? h - a.c.heads : h;
-        float v[16];
-        if (s_tile[tl] >= 0) {
-            load_block<FMT>(a.c.data + s_tile[tl] + hk * head_bytes, is_v, s_row[tl], j, D, is_v ? gv : gk, v);
-        } else {
+        const uint8_t* base = a.c.data + hk * head_bytes;
+        YT* out = (YT*)(is_v ? a.v_out : a.k_out) + t0 * y_ld + hk * D + j * 8;
+        const float gs = is_v ? gv : gk;
+        constexpr int batch = FMT == NVFP4_KV_BF16 ? kBatch : 2 * kBatch;
+        for (int tl0 = first; tl0 < nt; tl0 += batch * per) {
+            RawRun<FMT> x[batch][2] = {};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-        }
-        YT* yp = (YT*)(is_v ? a.v_out : a.k_out) + ((t0 + tl) * a.c.heads + hk) * D + j * 16;
-        float x[8], y[8];
+            for (int k = 0; k < batch; ++k) {
+                const int tl = tl0 + k * per;
+                const Slot s = s_slot[tl < nt ? tl : 0];
+                if (tl < nt && s.tile >= 0) {
+                    load_run<FMT, D>(base + s.tile, is_v, s, 8 * j, x[k][0]);
+                    load_run<FMT, D>(base + s.tile, is_v, s, D / 2 + 8 * j, x[k][1]);
+                }
+            }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = v[i];
-            y[i] = v[8 + i];
+            for (int k = 0; k < batch; ++k) {
+                const int tl = tl0 + k * per;
+                if (tl < nt) {
+                    float v[8];
+                    run_values<FMT>(x[k][0], gs, v);
+                    store8(out + tl * y_ld, v);
+                    run_values<FMT>(x[k][1], gs, v);
+                    store8(out + tl * y_ld + D / 2, v);
+                }
+            }
         }
-        store8(yp, x);
-        store8(yp + 8, y);
     }
 }
 
 // ---- launches ----------------------------------------------------------------
 
-// Tokens and heads of a CTA.  Few units in all: one per thread, one token per
-// CTA (latency).  Many: about four per thread and up to 16 tokens, so that
-// angles and addresses are shared.
-static void cta_shape(int64_t T, int heads, int units, int pairs, int& tt, int& hc) {
-    int per_thread = 1;
-    tt = 1;
-    if (T * heads * units > (int64_t)148 * 8 * kCtaThreads) {
-        per_thread = 4;
-        tt = pairs ? kCtaThreads / pairs : kMaxTokens;
-        tt = tt < 1 ? 1 : tt > kMaxTokens ? kMaxTokens : tt;
+// Tokens and heads of a CTA.  Where a warp per head and one pass of its lanes
+// leave the GPU unfilled (decode steps), that: latency counts.  Else four
+// passes, and as many heads as still leave about three CTAs per SM, so that
+// angles and slots are found once for all of them.
+static void cta_shape(int64_t T, int heads, int units, int& tt, int& hc) {
+    const int per = units < 32 ? 32 / units : 1;
+    tt = per;
+    hc = kWarps;
+    if ((T + tt - 1) / tt * ((heads + hc - 1) / hc) > 148 * 4) {
+        tt = per * kPasses;
+        const int64_t groups = (T + tt - 1) / tt;
+        while (hc < heads && groups * ((heads + 2 * hc - 1) / (2 * hc)) >= 148 * 16) hc *= 2;
     }
-    hc = (kCtaThreads * per_thread + tt * units - 1) / (tt * units);
-    if (hc < 1) hc = 1;
-    if (hc > heads) hc = heads;
 }
 
 static cudaLaunchConfig_t pdl_config(cudaLaunchAttribute* attr, int64_t T, int heads, int tt, int hc, size_t smem,
@@ -477,7 +613,7 @@ int launch_rope(const void* x, int x_dtype, int64_t T, int heads, int D, int64_t
                 int64_t y_ld, cudaStream_t st) {
     const RopeParams rp{positions, freqs, rot / 2, layout, mscale, inverse};
     int tt, hc;
-    cta_shape(T, heads, D / 16, rp.pairs, tt, hc);
+    cta_shape(T, heads, D / 16, tt, hc);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, T, heads, tt, hc, (size_t)(tt * rp.pairs) * sizeof(float2), st);
     cudaError_t e;
@@ -494,12 +630,20 @@ int launch_rope(const void* x, int x_dtype, int64_t T, int heads, int D, int64_t
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }
 
+template <typename XT, int FMT, bool ROPE>
+static cudaError_t kv_write_dim(cudaLaunchConfig_t& cfg, const KvWriteArgs& a) {
+    switch (a.c.head_dim) {
+        case 64: return cudaLaunchKernelEx(&cfg, kv_write_kernel<XT, FMT, 64, ROPE>, a);
+        case 128: return cudaLaunchKernelEx(&cfg, kv_write_kernel<XT, FMT, 128, ROPE>, a);
+        default: return cudaLaunchKernelEx(&cfg, kv_write_kernel<XT, FMT, 256, ROPE>, a);
+    }
+}
 template <typename XT, bool ROPE>
 static cudaError_t kv_write_fmt(cudaLaunchConfig_t& cfg, const KvWriteArgs& a) {
     switch (a.c.format) {
-        case NVFP4_KV_BF16: return cudaLaunchKernelEx(&cfg, kv_write_kernel<XT, NVFP4_KV_BF16, ROPE>, a);
-        case NVFP4_KV_E4M3: return cudaLaunchKernelEx(&cfg, kv_write_kernel<XT, NVFP4_KV_E4M3, ROPE>, a);
-        default: return cudaLaunchKernelEx(&cfg, kv_write_kernel<XT, NVFP4_KV_NVFP4, ROPE>, a);
+        case NVFP4_KV_BF16: return kv_write_dim<XT, NVFP4_KV_BF16, ROPE>(cfg, a);
+        case NVFP4_KV_E4M3: return kv_write_dim<XT, NVFP4_KV_E4M3, ROPE>(cfg, a);
+        default: return kv_write_dim<XT, NVFP4_KV_NVFP4, ROPE>(cfg, a);
     }
 }
 
@@ -514,7 +658,7 @@ int launch_kv_write(const KvView& c, const void* k, const void* v, int x_dtype, 
     a.T = T;
     a.slots = slots;
     a.status = status;
-    cta_shape(T, 2 * c.heads, c.head_dim / 16, 0, a.tt, a.hc);
+    cta_shape(T, 2 * c.heads, c.head_dim / 16, a.tt, a.hc);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, T, 2 * c.heads, a.tt, a.hc, 0, st);
     const cudaError_t e = x_dtype == NVFP4_DTYPE_BF16 ? kv_write_fmt<__nv_bfloat16, false>(cfg, a)
@@ -541,9 +685,10 @@ int launch_rope_kv_write(const KvView& c, const void* q, const void* k, const vo
     a.q_out = (__nv_bfloat16*)q_out;
     a.status = status;
     const int heads = q_heads + 2 * c.heads;
-    cta_shape(T, heads, c.head_dim / 16, a.rp.pairs, a.tt, a.hc);
-    const int staged_heads = a.hc < c.heads ? a.hc : c.heads;
-    const size_t smem = (size_t)(a.tt * a.rp.pairs) * sizeof(float2) + (size_t)a.tt * staged_heads * c.head_dim * 2;
+    cta_shape(T, heads, c.head_dim / 16, a.tt, a.hc);
+    // angles; for NVFP4 a batch of bf16 key rows per warp
+    const size_t rows = (size_t)kWarps * kBatch * (32 / (c.head_dim / 16)) * c.head_dim * 2;
+    const size_t smem = (size_t)(a.tt * a.rp.pairs) * sizeof(float2) + (c.format == NVFP4_KV_NVFP4 ? rows : 0);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, T, heads, a.tt, a.hc, smem, st);
     const cudaError_t e = x_dtype == NVFP4_DTYPE_BF16 ? kv_write_fmt<__nv_bfloat16, true>(cfg, a)
@@ -551,12 +696,20 @@ int launch_rope_kv_write(const KvView& c, const void* q, const void* k, const vo
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
 }
 
+template <typename YT, int FMT>
+static cudaError_t kv_read_dim(cudaLaunchConfig_t& cfg, const KvReadArgs& a) {
+    switch (a.c.head_dim) {
+        case 64: return cudaLaunchKernelEx(&cfg, kv_read_kernel<YT, FMT, 64>, a);
+        case 128: return cudaLaunchKernelEx(&cfg, kv_read_kernel<YT, FMT, 128>, a);
+        default: return cudaLaunchKernelEx(&cfg, kv_read_kernel<YT, FMT, 256>, a);
+    }
+}
 template <typename YT>
 static cudaError_t kv_read_fmt(cudaLaunchConfig_t& cfg, const KvReadArgs& a) {
     switch (a.c.format) {
-        case NVFP4_KV_BF16: return cudaLaunchKernelEx(&cfg, kv_read_kernel<YT, NVFP4_KV_BF16>, a);
-        case NVFP4_KV_E4M3: return cudaLaunchKernelEx(&cfg, kv_read_kernel<YT, NVFP4_KV_E4M3>, a);
-        default: return cudaLaunchKernelEx(&cfg, kv_read_kernel<YT, NVFP4_KV_NVFP4>, a);
+        case NVFP4_KV_BF16: return kv_read_dim<YT, NVFP4_KV_BF16>(cfg, a);
+        case NVFP4_KV_E4M3: return kv_read_dim<YT, NVFP4_KV_E4M3>(cfg, a);
+        default: return kv_read_dim<YT, NVFP4_KV_NVFP4>(cfg, a);
     }
 }
 
@@ -569,7 +722,7 @@ int launch_kv_read(const KvView& c, const int64_t* slots, int64_t T, void* k_out
     a.k_out = k_out;
     a.v_out = v_out;
     a.status = status;
-    cta_shape(T, 2 * c.heads, c.head_dim / 16, 0, a.tt, a.hc);
+    cta_shape(T, 2 * c.heads, c.head_dim / 16, a.tt, a.hc);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, T, 2 * c.heads, a.tt, a.hc, 0, st);
     const cudaError_t e =
