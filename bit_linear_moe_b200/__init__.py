@@ -398,19 +398,22 @@ def moe_layer_decode(h: torch.Tensor, w_router: torch.Tensor, k: int, gate_up, d
 # ---- rotary positions, the paged key-value cache, attention of one new token -------
 
 
-# The current stream's handle by device index (the public call builds a Stream object: 3 us
-# of a decode step's enqueue time).
+# These calls are made once per layer and step, so their enqueue time counts: the current
+# stream's handle and device come from the functions under the public ones (3 us for the
+# Stream object that torch.cuda.current_stream builds, 0.1 us here), and sizes are passed
+# to torch.empty one by one (a tuple costs it 0.7 us more).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _launch(dev: torch.device, name: str, *args):
+def _launch(dev: torch.device, name: str, args: tuple):
     """Call a C entry point on ``dev``'s current stream (made the current device for
     the call when it is not)."""
     index = dev.index
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         with torch.cuda.device(dev):
-            return _launch(dev, name, *args)
+            return _launch(dev, name, args)
     status = getattr(_lib or lib(), name)(*args, _raw_stream(index))
     if status != OK:
         raise NVFP4Error(status, name)
@@ -419,14 +422,18 @@ def _launch(dev: torch.device, name: str, *args):
 def _heads_view(t: torch.Tensor, dev, what: str, T=None, heads=None, head_dim=None) -> int:
     """Row stride (elements) of a ``[rows, heads, head_dim]`` view on ``dev`` whose heads
     are packed, as a slice of fused QKV rows is."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{what} must be a [rows, heads, head_dim] view with packed heads")
-    if T is not None and (shape[0] != T or shape[1] != heads or shape[2] != head_dim):
+    n, h, d = shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and h > 1):
+        raise ValueError(f"{what} must be a [rows, heads, head_dim] view with packed heads")
+    if T is not None and (n != T or h != heads or d != head_dim):
         raise ValueError(f"{what} must have shape {(T, heads, head_dim)}, not {tuple(shape)}")
     if t.device != dev:
         raise ValueError(f"{what} must be on {dev}, not {t.device}")
-    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
+    return s0 if n > 1 else h * d
 
 
 def _vector(t: torch.Tensor, dtype, n: int | None, dev, what: str) -> int:
@@ -504,13 +511,13 @@ def nvfp4_rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, la
     x_ld = _heads_view(x, dev, "x")
     T, heads, D = x.shape
     if y is None:
-        y = x.new_empty((T, heads, D), dtype=y_dtype)
+        y = torch.empty(T, heads, D, dtype=y_dtype, device=dev)
         y_ld = heads * D
     else:
         y_ld = _heads_view(y, dev, "y", T, heads, D)
-    _launch(dev, "nvfp4_rope", x.data_ptr(), _dtype_code(x), T, heads, D, x_ld,
+    _launch(dev, "nvfp4_rope", (x.data_ptr(), _dtype_code(x), T, heads, D, x_ld,
             _vector(positions, torch.int64, T, dev, "positions"), _vector(freqs, torch.float64, None, dev, "freqs"),
-            2 * freqs.numel(), layout, mscale, int(inverse), y.data_ptr(), _dtype_code(y), y_ld)
+            2 * freqs.numel(), layout, mscale, int(inverse), y.data_ptr(), _dtype_code(y), y_ld))
     return y
 
 
@@ -522,25 +529,24 @@ def nvfp4_kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torc
     k_ld, v_ld = _heads_view(k, dev, "k", T, heads, D), _heads_view(v, dev, "v", T, heads, D)
     if k.dtype != v.dtype:
         raise TypeError("k and v must have one dtype")
-    _launch(dev, "nvfp4_kv_write", cache._ref, k.data_ptr(), v.data_ptr(), _dtype_code(k), T, k_ld, v_ld,
-            _vector(slots, torch.int64, T, dev, "slots"))
+    _launch(dev, "nvfp4_kv_write", (cache._ref, k.data_ptr(), v.data_ptr(), _dtype_code(k), T, k_ld, v_ld,
+            _vector(slots, torch.int64, T, dev, "slots")))
 
 
 def nvfp4_kv_read(cache: KVCache, slots: torch.Tensor, k_out=None, v_out=None, y_dtype=torch.bfloat16):
     """The dequantized keys and values of ``slots [T]``: two ``[T, heads, head_dim]``
     tensors (bf16 or fp32); zeros for negative slots."""
     dev = cache.device
-    T = slots.numel()
-    shape = (T, cache.heads, cache.head_dim)
+    T, heads, D = slots.numel(), cache.heads, cache.head_dim
     if k_out is None:
-        k_out = cache.data.new_empty(shape, dtype=y_dtype if v_out is None else v_out.dtype)
+        k_out = torch.empty(T, heads, D, dtype=y_dtype if v_out is None else v_out.dtype, device=dev)
     if v_out is None:
-        v_out = cache.data.new_empty(shape, dtype=k_out.dtype)
+        v_out = torch.empty(T, heads, D, dtype=k_out.dtype, device=dev)
     if k_out.dtype != v_out.dtype:
         raise TypeError("k_out and v_out must have one dtype")
-    code, n = _dtype_code(k_out), T * cache.heads * cache.head_dim
-    _launch(dev, "nvfp4_kv_read", cache._ref, _vector(slots, torch.int64, T, dev, "slots"), T,
-            _vector(k_out, k_out.dtype, n, dev, "k_out"), _vector(v_out, v_out.dtype, n, dev, "v_out"), code)
+    code, n = _dtype_code(k_out), T * heads * D
+    _launch(dev, "nvfp4_kv_read", (cache._ref, _vector(slots, torch.int64, T, dev, "slots"), T,
+            _vector(k_out, k_out.dtype, n, dev, "k_out"), _vector(v_out, v_out.dtype, n, dev, "v_out"), code))
     return k_out, v_out
 
 
@@ -557,12 +563,12 @@ def nvfp4_rope_kv_write(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: tor
     if q.dtype != k.dtype or k.dtype != v.dtype:
         raise TypeError("q, k and v must have one dtype")
     if q_out is None:
-        q_out = q.new_empty((T, q_heads, D), dtype=torch.bfloat16)
-    _launch(dev, "nvfp4_rope_kv_write", cache._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), T,
+        q_out = torch.empty(T, q_heads, D, dtype=torch.bfloat16, device=dev)
+    _launch(dev, "nvfp4_rope_kv_write", (cache._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), T,
             q_heads, q_ld, k_ld, v_ld, _vector(positions, torch.int64, T, dev, "positions"),
             _vector(slots, torch.int64, T, dev, "slots"), _vector(freqs, torch.float64, None, dev, "freqs"),
             2 * freqs.numel(), layout, mscale,
-            _vector(q_out, torch.bfloat16, T * q_heads * D, dev, "q_out"))
+            _vector(q_out, torch.bfloat16, T * q_heads * D, dev, "q_out")))
     return q_out
 
 
@@ -587,17 +593,17 @@ def nvfp4_attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     max_pages = page_table.shape[1]
     table_ld = page_table.stride(0) if B > 1 else max_pages
     if y is None:
-        y = q.new_empty((B, q_heads, D), dtype=y_dtype)
+        y = torch.empty(B, q_heads, D, dtype=y_dtype, device=dev)
     y_ptr = _vector(y, y.dtype, B * q_heads * D, dev, "y")
     lse = torch.empty((B, q_heads), dtype=torch.float32, device=dev) if want_lse else None
     if ws is None:
         ws = torch.empty(nvfp4_attn_decode_workspace(cache, B, q_heads, max_pages), dtype=torch.uint8, device=dev)
     elif ws.device != dev or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on {dev}")
-    _launch(dev, "nvfp4_attn_decode", q.data_ptr(), B, q_heads, q_ld, cache._ref, page_table.data_ptr(), max_pages,
+    _launch(dev, "nvfp4_attn_decode", (q.data_ptr(), B, q_heads, q_ld, cache._ref, page_table.data_ptr(), max_pages,
             table_ld, _vector(seq_lens, torch.int32, B, dev, "seq_lens"), D ** -0.5 if scale is None else scale, window,
             y_ptr, _dtype_code(y), None if lse is None else lse.data_ptr(), ws.data_ptr(),
-            ws.numel() * ws.element_size())
+            ws.numel() * ws.element_size()))
     return y if lse is None else (y, lse)
 
 
