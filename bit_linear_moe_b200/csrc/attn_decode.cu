@@ -29,7 +29,7 @@ static bool plan(const KvView& c, int64_t B, int q_heads, int64_t max_pages, Pla
     p.shape.grid = (tiles + 3) / 4 < most ? (tiles + 3) / 4 : most;
     p.shape.seg_tiles = max_pages * (c.page_size / kKvTile);
     p.header = ((size_t)(B + 2) * 4 + 255) / 256 * 256;
-    p.bytes = p.header + (size_t)p.shape.grid * 2 * p.cols * (c.head_dim + 2) * 4;
+    p.bytes = p.header + (size_t)p.shape.grid * 2 * (p.cols * (c.head_dim + 4) + 3) / 4 * 4 * 4;
     return true;
 }
 

@@ -72,11 +72,15 @@ struct Shape {
 // Up to this many tiles per warp a cluster per segment is used.
 constexpr int64_t kSegmentTiles = 16;
 
-// A piece: O [cols][D], then m [cols] (log2 units), then l [cols].
+// A piece: O [cols] rows of D (kLd apart: the fragments' stores, 16 elements
+// apart from lane group to lane group and two columns from lane to lane, would
+// meet in two banks without the two floats of padding), then m [cols] (log2
+// units), then l [cols].
 template <int D, int NT>
 struct Piece {
-    static constexpr int kCols = 8 * NT;
-    static constexpr int kFloats = kCols * (D + 2);
+    static constexpr int kCols = 8 * NT, kLd = D + 2;
+    static constexpr int kMax = kCols * kLd, kSum = kMax + kCols;
+    static constexpr int kFloats = (kSum + kCols + 3) / 4 * 4;
 };
 
 template <int FMT, int D, int NT>
@@ -590,7 +594,7 @@ struct Warp {
     }
     NVFP4_DEV void write_piece(float* dst) const {
         const int lane = threadIdx.x & 31, t = lane & 3;
-        constexpr int cols = 8 * NT;
+        using P = Piece<D, NT>;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -598,11 +602,11 @@ struct Warp {
                 const int col = n * 8 + 2 * t + c;
 #pragma unroll
                 for (int mt = 0; mt < C::kMt; ++mt)
-                    *reinterpret_cast<float2*>(dst + col * D + column(mt)) =
+                    *reinterpret_cast<float2*>(dst + col * P::kLd + column(mt)) =
                         make_float2(o[n][mt][c], o[n][mt][2 + c]);
                 if (lane < 4) {
-                    dst[cols * D + col] = m[n][c];
-                    dst[cols * D + cols + col] = l[n][c];
+                    dst[P::kMax + col] = m[n][c];
+                    dst[P::kSum + col] = l[n][c];
                 }
             }
     }
@@ -680,32 +684,66 @@ struct Joined {
     static constexpr int kV = D / 32;
     float v[kV], M, L;
 
-    // Pieces p with bit p of `set` (p < P), at piece(p) in shared memory.
-    template <int NT, int P, typename F>
+    // Pieces p with bit p of `set` (p < P; kAll: every p), at piece(p) in shared memory.
+    template <int NT, int P, bool kAll, typename F>
     NVFP4_DEV void join(F piece, uint32_t set, int col) {
-        constexpr int kCols = 8 * NT;
+        using Pc = Piece<D, NT>;
         const int lane = threadIdx.x & 31;
         const bool in = lane < P && (set >> lane & 1);
-        const float* mine = piece(in ? lane : __ffs(set) - 1) + kCols * D + col;
+        const float* mine = piece(in ? lane : __ffs(set) - 1) + Pc::kMax + col;
         const float m = in ? mine[0] : __int_as_float(0xff800000);
         M = warp_max(m);
         const float w = in ? weight(m, M) : 0.0f;
-        L = warp_sum(in ? w * mine[kCols] : 0.0f);
+        L = warp_sum(in ? w * mine[Pc::kCols] : 0.0f);
 #pragma unroll
         for (int k = 0; k < kV; ++k) v[k] = 0.0f;
-        const float* base = nullptr;
-#pragma unroll 4
+#pragma unroll
         for (int p = 0; p < P; ++p) {
-            if (!(set >> p & 1)) continue;
-            base = piece(p) + col * D + lane * kV;
+            if (!kAll && !(set >> p & 1)) continue;
+            const float* src = piece(p) + col * Pc::kLd + lane * kV;
             const float wp = __shfl_sync(0xffffffffu, w, p);
 #pragma unroll
             for (int k = 0; k < kV; k += 2) {
-                const float2 x = *reinterpret_cast<const float2*>(base + k);
+                const float2 x = *reinterpret_cast<const float2*>(src + k);
                 v[k] += wp * x.x;
                 v[k + 1] += wp * x.y;
             }
         }
+    }
+
+    // The pieces of a cluster's CTAs, each at the same place in its shared memory.
+    template <int NT>
+    NVFP4_DEV void join_cluster(const float* mine, int cluster, int col) {
+        using Pc = Piece<D, NT>;
+        const int lane = threadIdx.x & 31;
+        float m = __int_as_float(0xff800000), l = 0.0f;
+        if (lane < cluster) {
+            m = ld_dsmem_f32(mine + Pc::kMax + col, (uint32_t)lane);
+            l = ld_dsmem_f32(mine + Pc::kSum + col, (uint32_t)lane);
+        }
+        float2 x[8][kV / 2];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < cluster) {
+#pragma unroll
+                for (int k = 0; k < kV / 2; ++k)
+                    x[c][k] = ld_dsmem_f32x2(mine + col * Pc::kLd + lane * kV + 2 * k, (uint32_t)c);
+            }
+        M = warp_max(m);
+        const float w = weight(m, M);
+        L = warp_sum(w * l);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) v[k] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < cluster) {
+                const float wc = __shfl_sync(0xffffffffu, w, c);
+#pragma unroll
+                for (int k = 0; k < kV / 2; ++k) {
+                    v[2 * k] += wc * x[c][k].x;
+                    v[2 * k + 1] += wc * x[c][k].y;
+                }
+            }
     }
 
     template <typename YT>
@@ -722,14 +760,14 @@ struct Joined {
 
     template <int NT>
     NVFP4_DEV void store_piece(float* part, int col) const {
-        constexpr int kCols = 8 * NT;
+        using Pc = Piece<D, NT>;
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int k = 0; k < kV; k += 2)
-            *reinterpret_cast<float2*>(part + col * D + lane * kV + k) = make_float2(v[k], v[k + 1]);
+            *reinterpret_cast<float2*>(part + col * Pc::kLd + lane * kV + k) = make_float2(v[k], v[k + 1]);
         if (lane == 0) {
-            part[kCols * D + col] = M;
-            part[kCols * D + kCols + col] = L;
+            part[Pc::kMax + col] = M;
+            part[Pc::kSum + col] = L;
         }
     }
 };
@@ -924,7 +962,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
         const uint32_t id = __shfl_sync(0xffffffffu, my_seg, lead), set = __shfl_sync(0xffffffffu, same, lead);
         const uint4 ds = s_desc[lead];
         Joined<D> r;
-        r.template join<NT, 2 * W>(piece, set, col);
+        if ((int)ds.w * kCols + col >= a.G) continue;  // a column of padding
+        r.template join<NT, 2 * W, false>(piece, set, col);
         if (id >= t0 && id + ds.x <= t1) r.template store_output<YT>(a, ds.y, ds.z, ds.w * kCols + col);
         else r.template store_piece<NT>(a.partial + ((int64_t)blockIdx.x * 2 + (id >= t0 ? 1 : 0)) * Piece<D, NT>::kFloats, col);
     }
@@ -1022,48 +1061,25 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
         return reinterpret_cast<const float*>(smem + (size_t)p * S * C::kTile);
     };
     const uint32_t set = (1u << W) - 1;
+    const int live = min(kCols, a.G - (int)chunk * kCols);  // columns that are not padding
     if (cluster == 1) {
-        for (int col = warp; col < kCols; col += W) {
+        for (int col = warp; col < live; col += W) {
             Joined<D> r;
-            r.template join<NT, W>(piece, set, col);
+            r.template join<NT, W, true>(piece, set, col);
             r.template store_output<YT>(a, b, hk, (int)chunk * kCols + col);
         }
         return;
     }
-    for (int col = warp; col < kCols; col += W) {
+    for (int col = warp; col < live; col += W) {
         Joined<D> r;
-        r.template join<NT, W>(piece, set, col);
+        r.template join<NT, W, true>(piece, set, col);
         r.template store_piece<NT>(joined, col);
     }
     cluster_sync();
-    // the cluster's CTAs share the columns; a lane reads its elements of every
-    // CTA's piece
-    for (int col = (int)rank + cluster * warp; col < kCols; col += cluster * W) {
+    // the cluster's CTAs share the columns
+    for (int col = (int)rank + cluster * warp; col < live; col += cluster * W) {
         Joined<D> r;
-        float m[8], l[8];
-        r.M = __int_as_float(0xff800000);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            m[c] = __int_as_float(0xff800000);
-            l[c] = 0.0f;
-            if (c < cluster) {
-                m[c] = ld_dsmem_f32(joined + kCols * D + col, (uint32_t)c);
-                l[c] = ld_dsmem_f32(joined + kCols * D + kCols + col, (uint32_t)c);
-            }
-            r.M = fmaxf(r.M, m[c]);
-        }
-        r.L = 0.0f;
-#pragma unroll
-        for (int k = 0; k < Joined<D>::kV; ++k) r.v[k] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            if (c >= cluster) break;
-            const float w = weight(m[c], r.M);
-            r.L += w * l[c];
-#pragma unroll
-            for (int k = 0; k < Joined<D>::kV; ++k)
-                r.v[k] += w * ld_dsmem_f32(joined + col * D + lane * Joined<D>::kV + k, (uint32_t)c);
-        }
+        r.template join_cluster<NT>(joined, cluster, col);
         r.template store_output<YT>(a, b, hk, (int)chunk * kCols + col);
     }
     cluster_sync();  // pieces stay until every CTA has read them
@@ -1096,10 +1112,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const Args a) {
     const uint32_t c0 = ts / per, c1 = (ts + tiles - 1) / per;
     if (c0 == c1) return;
     const int step = kRows == 1 ? 8 : 1, off = kRows == 1 ? warp : 0;
-    auto part = [&](uint32_t c) { return a.partial + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * Piece<D, NT>::kFloats; };
+    using Pc = Piece<D, NT>;
+    auto part = [&](uint32_t c) { return a.partial + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * Pc::kFloats; };
     // maximum over the pieces, lanes striding over them
     float M = __int_as_float(0xff800000);
-    for (uint32_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c)[kCols * D + col]);
+    for (uint32_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c)[Pc::kMax + col]);
     M = warp_max(M);
     float v[kV], L = 0.0f;
 #pragma unroll
@@ -1107,10 +1124,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const Args a) {
 #pragma unroll 4
     for (uint32_t c = c0 + off; c <= c1; c += step) {
         const float* src = part(c);
-        const float w = weight(src[kCols * D + col], M);
-        L += w * src[kCols * D + kCols + col];
+        const float w = weight(src[Pc::kMax + col], M);
+        L += w * src[Pc::kSum + col];
 #pragma unroll
-        for (int k = 0; k < kV; ++k) v[k] += w * src[col * D + lane + 32 * k];
+        for (int k = 0; k < kV; ++k) v[k] += w * src[col * Pc::kLd + lane + 32 * k];
     }
     if constexpr (kRows == 1) {
         __shared__ float s_v[8][D + 1];

@@ -151,6 +151,13 @@ NVFP4_DEV float ld_dsmem_f32(const float* local, uint32_t rank) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
     return v;
 }
+NVFP4_DEV float2 ld_dsmem_f32x2(const float* local, uint32_t rank) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(remote) : "memory");
+    return v;
+}
 
 // ---- host: tensor maps -------------------------------------------------------
 // 2D row-major byte matrix [rows, row_bytes] (row stride = row_bytes), box of
