@@ -143,18 +143,28 @@ NVFP4_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, ui
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// N bytes (4, 8 or 16) of shared memory as words.
+// Shared memory by its 32-bit address (volatile: stays behind the barrier wait).
+// N bytes (4, 8 or 16) as words.
 template <int N>
-NVFP4_DEV void lds(const uint8_t* p, uint32_t (&w)[N / 4]) {
-    if constexpr (N == 16) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else if constexpr (N == 8) {
-        const uint2 v = *reinterpret_cast<const uint2*>(p);
-        w[0] = v.x, w[1] = v.y;
-    } else {
-        w[0] = *reinterpret_cast<const uint32_t*>(p);
-    }
+NVFP4_DEV void lds(uint32_t p, uint32_t (&w)[N / 4]) {
+    if constexpr (N == 16)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(p));
+    else if constexpr (N == 8)
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p));
+    else
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(p));
+}
+NVFP4_DEV uint32_t lds_u16(uint32_t p) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p));
+    return v;
+}
+NVFP4_DEV uint32_t lds_u8(uint32_t p) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(p));
+    return v;
 }
 
 // Where a tile of the list lies.
@@ -309,10 +319,10 @@ struct Warp {
     }
 
     // Block scale bytes of a key row's unit -> fp16 pairs (s, s), one per block.
-    static NVFP4_DEV void key_scale(const uint8_t* p, uint32_t (&sc)[2]) {
+    static NVFP4_DEV void key_scale(uint32_t p, uint32_t (&sc)[2]) {
         uint32_t h;
-        if constexpr (kUk == 16) h = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(p));
-        else h = e4m3x2_to_f16x2(*p);
+        if constexpr (kUk == 16) h = e4m3x2_to_f16x2((uint16_t)lds_u16(p));
+        else h = e4m3x2_to_f16x2((uint16_t)lds_u8(p));
         sc[0] = prmt(h, h, 0x1010);
         sc[1] = prmt(h, h, 0x3232);
     }
@@ -320,7 +330,7 @@ struct Warp {
     // kStep tiles with tokens tok0 .. tok0 + 16 kStep - 1 at tp[0], tp[1]; tokens
     // outside [lo, hi) are masked (their bytes may be anything, NaN included).
     static constexpr int kStep = C::kStep;
-    NVFP4_DEV void tiles(const uint8_t* const (&tp)[kStep], int tok0, int lo, int hi) {
+    NVFP4_DEV void tiles(const uint32_t (&tp)[kStep], int tok0, int lo, int hi) {
         const bool edge = tok0 < lo || tok0 + kStep * kKvTile > hi;
         const int lane = threadIdx.x & 31, g = lane >> 2;
         float s[kStep][NT][4];
@@ -401,9 +411,9 @@ struct Warp {
     }
 
     // S^T = K Q^T of a tile (before the factor): this thread's rows g and g + 8.
-    NVFP4_DEV void scores(const uint8_t* tp, float (&sum)[NT][4]) {
+    NVFP4_DEV void scores(uint32_t tp, float (&sum)[NT][4]) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        const uint8_t* ks = tp + 32 * C::kDb;  // key scales, then value scales
+        const uint32_t ks = tp + 32 * C::kDb;  // key scales, then value scales
         float s[NT][2][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -420,7 +430,7 @@ struct Warp {
             lds<kUk>(tp + g * C::kDb + at, w0);
             lds<kUk>(tp + (g + 8) * C::kDb + at, w1);
             if constexpr (FMT == NVFP4_KV_NVFP4) {
-                const uint8_t* sp = ks + g * C::kSb + (off >> 3);
+                const uint32_t sp = ks + g * C::kSb + (off >> 3);
                 uint32_t sc0[2], sc1[2];
                 key_scale(sp, sc0);
                 key_scale(sp + 8 * C::kSb, sc1);
@@ -472,13 +482,12 @@ struct Warp {
     }
 
     // O^T += V^T P^T of a tile.
-    NVFP4_DEV void values(const uint8_t* tp, bool edge, int tok0, int lo, int len, const uint32_t (&ph)[NT][2],
+    NVFP4_DEV void values(uint32_t tp, bool edge, int tok0, int lo, int len, const uint32_t (&ph)[NT][2],
                           const uint32_t (&pl)[NT][2]) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        const uint8_t* ks = tp + 32 * C::kDb;
+        const uint32_t ks = tp + 32 * C::kDb;
         // ---- O^T += V^T P^T: this thread's columns of tokens 2t, 2t + 1, 2t + 8, 2t + 9
-        const uint8_t* vp = tp + 16 * C::kDb;
-        const uint8_t* vs = ks + 16 * C::kSb;
+        const uint32_t vp = tp + 16 * C::kDb, vs = ks + 16 * C::kSb;
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
             const int off = kUv * (g + 8 * i);
@@ -489,9 +498,9 @@ struct Warp {
                 const int r = 2 * t + (k & 1) + 8 * (k >> 1);
                 lds<kUv>(vp + r * C::kDb + kv_place(r, off, C::kPieces), w[k]);
                 if constexpr (FMT == NVFP4_KV_NVFP4) {
-                    const uint8_t* sp = vs + r * C::kSb + (off >> 3);
-                    if constexpr (kUv == 16) sb[k] = *reinterpret_cast<const uint16_t*>(sp);
-                    else sb[k] = *sp;
+                    const uint32_t sp = vs + r * C::kSb + (off >> 3);
+                    if constexpr (kUv == 16) sb[k] = lds_u16(sp);
+                    else sb[k] = lds_u8(sp);
                 }
             }
             if (edge) {
@@ -651,15 +660,15 @@ struct Step {
 };
 template <int kStep, int S>
 NVFP4_DEV Step<S> wait_tiles(const uint8_t* ring, int tile, uint64_t* full, uint32_t slot, uint32_t phase,
-                             uint32_t count, int* status, const uint8_t* (&tp)[kStep]) {
+                             uint32_t count, int* status, uint32_t (&tp)[kStep]) {
     Step<S> r;
     bool ok = mbar_wait(&full[slot], phase, status);
-    tp[0] = ring + slot * tile;
+    tp[0] = smem_u32(ring) + slot * tile;
     uint32_t next = slot + 1, ph = phase;
     if (next == (uint32_t)S) next = 0, ph ^= 1;
     r.second = next;
     if constexpr (kStep == 2) {
-        tp[1] = ring + next * tile;
+        tp[1] = smem_u32(ring) + next * tile;
         if (count == 2) {
             ok = mbar_wait(&full[next], ph, status) && ok;
             if (++next == (uint32_t)S) next = 0, ph ^= 1;
@@ -892,7 +901,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
         for (uint32_t i = 0; i < n_warp;) {
             // this step's tiles: up to kStep, of one segment
             const uint32_t count = min((uint32_t)C::kStep, min(n_warp - i, at.tiles - at.j));
-            const uint8_t* tp[C::kStep];
+            uint32_t tp[C::kStep];
             const Step<S> step = wait_tiles<C::kStep, S>(ring, C::kTile, full, slot, phase, count, a.status, tp);
             if (!step.ok) {
                 drain<S>(full, i, n_warp, a.status);
@@ -1033,7 +1042,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
     int tok0 = (int)j0 * kKvTile;
     for (uint32_t i = 0; i < n_warp;) {
         const uint32_t count = min((uint32_t)C::kStep, n_warp - i);
-        const uint8_t* tp[C::kStep];
+        uint32_t tp[C::kStep];
         const Step<S> step = wait_tiles<C::kStep, S>(ring, C::kTile, full, slot, phase, count, a.status, tp);
         if (!step.ok) {
             drain<S>(full, i, n_warp, a.status);
