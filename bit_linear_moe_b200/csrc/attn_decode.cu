@@ -22,13 +22,15 @@ static bool plan(const KvView& c, int64_t B, int q_heads, int64_t max_pages, Pla
     p.G = q_heads / c.heads;
     p.cols = cols_of(p.G, c.head_dim);
     p.chunks = (p.G + p.cols - 1) / p.cols;
-    const int64_t per_seq = (int64_t)c.heads * ((p.G + 7) / 8) * (c.page_size / kKvTile);
-    if (max_pages > (int64_t)0x7fffffff / per_seq / B || max_pages > (int64_t)0x7fffffff / c.page_size) return false;
+    // list positions are 32-bit: tiles and the cost of segments
+    if (max_pages > (int64_t)0x7fffffff / c.page_size) return false;
+    const int64_t seg = max_pages * (c.page_size / kKvTile) + kSegmentCost;
+    if (seg > (int64_t)0x7fffffff / ((int64_t)c.heads * ((p.G + 7) / 8)) / B) return false;
     const int64_t tiles = B * max_pages * c.heads * p.chunks * (c.page_size / kKvTile);
     const int64_t most = kv_tile_bytes(c.format, c.head_dim) >= 16384 ? kMaxGrid / kCtasPerSm : kMaxGrid;
     p.shape.grid = (tiles + 3) / 4 < most ? (tiles + 3) / 4 : most;
     p.shape.seg_tiles = max_pages * (c.page_size / kKvTile);
-    p.header = ((size_t)(B + 2) * 4 + 255) / 256 * 256;
+    p.header = ((size_t)(2 * B + 4) * 4 + 255) / 256 * 256;
     p.bytes = p.header + (size_t)p.shape.grid * 2 * (p.cols * (c.head_dim + 4) + 3) / 4 * 4 * 4;
     return true;
 }

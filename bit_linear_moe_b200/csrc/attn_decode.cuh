@@ -23,7 +23,9 @@
 //
 // Work split.  All tiles of all (sequence, key head, block of query columns)
 // segments form one list; every CTA takes an equal contiguous range of it and
-// every warp an equal range of that, whatever the lengths in the batch.  A
+// every warp an equal range of that, whatever the lengths in the batch.  (Equal
+// in cost: a segment counts kSegmentCost tiles more than it has, so that a
+// warp does not get a dozen one-tile segments.)  A
 // warp streams its tiles through a ring of its own (one bulk copy per tile,
 // S in flight) with its running maximum, sum and O^T in registers, and never
 // meets another warp until the end.  Segments that lie inside a warp are
@@ -58,7 +60,7 @@ struct Args {
     int window;        // 0: all
     void* y;           // [B, q_heads, D]
     float* lse;        // [B, q_heads] or null
-    uint32_t* header;  // workspace: [0] tiles per CTA, [1 .. B + 1] first tile of each sequence
+    uint32_t* header;  // workspace: [0] cost per CTA, then the list (see List)
     float* partial;    // workspace: [grid][2] pieces
     int* status;
     uint32_t zero;     // always 0 (see refill)
@@ -71,6 +73,9 @@ struct Shape {
 };
 // Up to this many tiles per warp a cluster per segment is used.
 constexpr int64_t kSegmentTiles = 16;
+// What beginning and ending a segment costs a warp, in tiles (measured: 2 x
+// the 2,000 cycles of an NVFP4 tile at D = 128).
+constexpr uint32_t kSegmentCost = 2;
 
 // A piece: O [cols] rows of D (kLd apart: the fragments' stores, 16 elements
 // apart from lane group to lane group and two columns from lane to lane, would
@@ -172,22 +177,42 @@ struct Place {
     uint32_t b, s, j, tiles;  // sequence, segment of it (key head, chunk), tile of the seen ones, their number
 };
 
-NVFP4_DEV Place place_of(uint32_t t, uint32_t hc, const uint32_t* first, uint32_t B) {
-    const uint32_t u = t / hc;
-    uint32_t lo = 0, hi = B;  // first[lo] <= u < first[hi]
-    while (hi - lo > 1) {
-        const uint32_t mid = (lo + hi) >> 1;
-        if (first[mid] <= u) lo = mid;
-        else hi = mid;
+// The list of all tiles: sequence b's hc segments begin at tile hc * first[b];
+// rank[b] non-empty sequences come before it.  The list's cost positions count
+// kSegmentCost more for every segment.
+struct List {
+    const uint32_t *first, *rank;  // [B + 1] each
+    uint32_t B, hc;
+    // sequence with at(b) <= u < at(b + 1)
+    template <typename F>
+    NVFP4_DEV uint32_t find(uint32_t u, F at) const {
+        uint32_t lo = 0, hi = B;
+        while (hi - lo > 1) {
+            const uint32_t mid = (lo + hi) >> 1;
+            if (at(mid) <= u) lo = mid;
+            else hi = mid;
+        }
+        return lo;
     }
-    Place p;
-    p.b = lo;
-    p.tiles = first[lo + 1] - first[lo];
-    const uint32_t rem = t - first[lo] * hc;
-    p.s = rem / p.tiles;
-    p.j = rem - p.s * p.tiles;
-    return p;
-}
+    NVFP4_DEV uint32_t cost_at(uint32_t b) const { return hc * (first[b] + kSegmentCost * rank[b]); }
+    // Where tile t of the list is.
+    NVFP4_DEV Place place_of(uint32_t t) const {
+        Place p;
+        p.b = find(t / hc, [&](uint32_t b) { return first[b]; });
+        p.tiles = first[p.b + 1] - first[p.b];
+        const uint32_t rem = t - first[p.b] * hc;
+        p.s = rem / p.tiles;
+        p.j = rem - p.s * p.tiles;
+        return p;
+    }
+    // The tiles before cost position u.
+    NVFP4_DEV uint32_t tiles_before(uint32_t u) const {
+        if (u >= cost_at(B)) return hc * first[B];
+        const uint32_t b = find(u, [&](uint32_t k) { return cost_at(k); });
+        const uint32_t tiles = first[b + 1] - first[b], rem = u - cost_at(b), s = rem / (tiles + kSegmentCost);
+        return hc * first[b] + s * tiles + min(rem - s * (tiles + kSegmentCost), tiles);
+    }
+};
 
 // Seen tokens of a sequence: [lo, len).
 NVFP4_DEV void seen_range(const Args& a, int b, int& lo, int& len) {
@@ -789,9 +814,11 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* ring_all = smem;
     float* pieces = reinterpret_cast<float*>(smem + C::kRingBytes);
-    uint32_t* first = reinterpret_cast<uint32_t*>(smem + C::kFixed);  // [B + 1]
+    uint32_t* first = reinterpret_cast<uint32_t*>(smem + C::kFixed);  // [B + 1] (List), then rank
+    uint32_t* rank_of = first + a.B + 1;
     __shared__ uint64_t s_full[W][S];
-    __shared__ uint32_t s_seg[2 * W], s_scan[W];
+    __shared__ uint32_t s_seg[2 * W];
+    __shared__ uint2 s_scan[W];
     __shared__ uint4 s_desc[2 * W];  // of a stored piece: tiles, sequence, key head, chunk
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -805,7 +832,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
 
     // ---- the list: first tile of each sequence (in tiles of one segment)
     const uint32_t B = (uint32_t)a.B;
-    uint32_t carry = 0;
+    uint32_t tiles_so_far = 0, seqs_so_far = 0;
     for (uint32_t b0 = 0; b0 < B; b0 += W * 32) {
         const uint32_t b = b0 + threadIdx.x;
         uint32_t n = 0;
@@ -816,38 +843,48 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
             n = len > lo ? (uint32_t)((len + kKvTile - 1) / kKvTile - lo / kKvTile) : 0u;
         }
         uint32_t x = n;
+        const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
             if (lane >= d) x += y;
         }
-        if (lane == 31) s_scan[warp] = x;
+        if (lane == 31) s_scan[warp] = make_uint2(x, (uint32_t)__popc(some));
         __syncthreads();
-        uint32_t before = carry, all = 0;
+        uint32_t before = tiles_so_far, rank = seqs_so_far + __popc(some & ((1u << lane) - 1));
         for (int w = 0; w < W; ++w) {
-            const uint32_t v = s_scan[w];
-            if (w < warp) before += v;
-            all += v;
+            const uint2 v = s_scan[w];
+            if (w < warp) before += v.x, rank += v.y;
+            tiles_so_far += v.x;
+            seqs_so_far += v.y;
         }
-        if (b < B) first[b] = before + x - n;
-        carry += all;
+        if (b < B) {
+            first[b] = before + x - n;
+            rank_of[b] = rank;
+        }
         __syncthreads();
     }
-    if (threadIdx.x == 0) first[B] = carry;
+    if (threadIdx.x == 0) {
+        first[B] = tiles_so_far;
+        rank_of[B] = seqs_so_far;
+    }
     __syncthreads();
 
     const uint32_t hc = (uint32_t)(a.c.heads * a.chunks);
-    const uint32_t total = carry * hc;
-    uint32_t per_cta = (total + gridDim.x - 1) / gridDim.x;
+    const List list{first, rank_of, B, hc};
+    const uint32_t cost = list.cost_at(B);
+    uint32_t per_cta = (cost + gridDim.x - 1) / gridDim.x;
     if (per_cta < (uint32_t)W) per_cta = W;
     if (blockIdx.x == 0) {
         if (threadIdx.x == 0) a.header[0] = per_cta;
-        for (uint32_t b = threadIdx.x; b <= B; b += W * 32) a.header[1 + b] = first[b];
+        for (uint32_t b = threadIdx.x; b < 2 * (B + 1); b += W * 32) a.header[1 + b] = first[b];
     }
-    const uint32_t t0 = min(total, per_cta * blockIdx.x), t1 = min(total, t0 + per_cta);
-    const uint32_t n_cta = t1 - t0;
-    const uint32_t w0 = t0 + (n_cta / W) * warp + min(n_cta % W, (uint32_t)warp);
-    const uint32_t n_warp = n_cta / W + ((uint32_t)warp < n_cta % W ? 1u : 0u);
+    // this CTA's and this warp's ranges of cost, then of tiles
+    const uint32_t u0 = min(cost, per_cta * blockIdx.x), u1 = min(cost, u0 + per_cta), n_cta = u1 - u0;
+    const uint32_t t0 = list.tiles_before(u0), t1 = list.tiles_before(u1);
+    const uint32_t wu0 = u0 + (n_cta / W) * warp + min(n_cta % W, (uint32_t)warp);
+    const uint32_t wu1 = wu0 + n_cta / W + ((uint32_t)warp < n_cta % W ? 1u : 0u);
+    const uint32_t w0 = list.tiles_before(wu0), n_warp = list.tiles_before(wu1) - w0;
 
     // ---- this warp's tiles
     uint8_t* ring = ring_all + (size_t)warp * S * C::kTile;
@@ -863,7 +900,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
             if (i < n_warp) {
                 Place p = pl;
                 p.j += i - pl_i;
-                if (p.j >= p.tiles) p = place_of(w0 + i, hc, first, B);
+                if (p.j >= p.tiles) p = list.place_of(w0 + i);
                 int lo, len;
                 seen_range(a, (int)p.b, lo, len);
                 const uint32_t jt = (uint32_t)(lo / kKvTile) + p.j;
@@ -880,7 +917,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, NT>::kWarps * 32, Cfg<FMT, D, NT>:
                 bulk_load(ring + slot * C::kTile, addr, bytes, &full[slot]);
             }
         };
-        Place at = place_of(w0, hc, first, B);
+        Place at = list.place_of(w0);
         uint32_t hk = at.s / (uint32_t)a.chunks, chunk = at.s - hk * (uint32_t)a.chunks;
         Warp<FMT, D, NT, YT> wk;
         wk.fetch_q(a, (int)at.b, (int)hk, (int)chunk);  // on their way while the page table is read
@@ -1108,7 +1145,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const Args a) {
     if (row >= (int64_t)a.B * a.q_heads) return;
     const int b = (int)(row / a.q_heads), hq = (int)(row - (int64_t)b * a.q_heads);
     const int hk = hq / a.G, gq = hq - hk * a.G, chunk = gq / kCols, col = gq - chunk * kCols;
-    const uint32_t per = a.header[0], f0 = a.header[1 + b], f1 = a.header[2 + b];
+    const uint32_t per = a.header[0], f0 = a.header[1 + b], f1 = a.header[2 + b], rank = a.header[2 + a.B + b];
     const uint32_t tiles = f1 - f0, hc = (uint32_t)(a.c.heads * a.chunks);
     YT* yp = (YT*)a.y + row * D;
     if (tiles == 0) {
@@ -1117,7 +1154,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const Args a) {
         if (a.lse && lane == 0) a.lse[row] = __int_as_float(0xff800000);
         return;
     }
-    const uint32_t ts = f0 * hc + (uint32_t)(hk * a.chunks + chunk) * tiles;
+    const uint32_t ts = hc * (f0 + kSegmentCost * rank) + (uint32_t)(hk * a.chunks + chunk) * (tiles + kSegmentCost);
     const uint32_t c0 = ts / per, c1 = (ts + tiles - 1) / per;
     if (c0 == c1) return;
     const int step = kRows == 1 ? 8 : 1, off = kRows == 1 ? warp : 0;
@@ -1226,9 +1263,9 @@ static int run(const Args& a, const Shape& sh, cudaStream_t st) {
     }
     static std::atomic<uint64_t> done{0};
     constexpr int kMostB = 4096;
-    if (!allow_smem(attn_decode_kernel<FMT, D, NT, YT>, done, C::kFixed + (kMostB + 4) * 4 + 16)) return NVFP4_ERR_LAUNCH;
+    if (!allow_smem(attn_decode_kernel<FMT, D, NT, YT>, done, C::kFixed + (kMostB + 2) * 8)) return NVFP4_ERR_LAUNCH;
     cfg.gridDim = dim3((unsigned)sh.grid);
-    cfg.dynamicSmemBytes = (size_t)C::kFixed + (size_t)((a.B + 4) / 4 * 4) * 4 + 16;
+    cfg.dynamicSmemBytes = (size_t)C::kFixed + (size_t)(a.B + 2) * 8;
     if (cudaLaunchKernelEx(&cfg, attn_decode_kernel<FMT, D, NT, YT>, a) != cudaSuccess) return NVFP4_ERR_LAUNCH;
     return run_join<D, NT, YT>(a, sh.grid, st);
 }

@@ -590,8 +590,8 @@ int nvfp4_rope_kv_write(const nvfp4_kv_cache* cache, const void* q, const void* 
  * does not depend on anything but the arguments' shapes and values: the same
  * call gives the same bits.
  * Requires 1 <= B <= 4096, q_heads a multiple of cache->heads, max_pages >= 1,
- * at most 2^31 - 1 tiles of 16 tokens in all (B * max_pages * page_size / 16 *
- * heads * ceil(q_heads / heads / 8)), q and y 16-byte aligned, q_ld % 8 == 0. */
+ * B * heads * ceil(q_heads / heads / 8) * (max_pages * page_size / 16 + 2) and
+ * max_pages * page_size below 2^31, q and y 16-byte aligned, q_ld % 8 == 0. */
 size_t nvfp4_attn_decode_workspace(const nvfp4_kv_cache* cache, int64_t B, int32_t q_heads, int64_t max_pages);
 int nvfp4_attn_decode(const void* q, int64_t B, int32_t q_heads, int64_t q_ld, const nvfp4_kv_cache* cache,
                       const int32_t* page_table, int64_t max_pages, int64_t table_ld, const int32_t* seq_lens,
