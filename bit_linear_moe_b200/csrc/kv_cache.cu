@@ -13,7 +13,7 @@
 // times an fp32 frequency would lose the angle: 2^20 * 2^-24 turns), its
 // fraction is exact, and cos and sin of it are fp64, rounded once to fp32.
 // B200 runs fp64 at half the fp32 rate and a CTA computes each angle once for
-// all of its heads, so this costs less than a table would cost in reads.  The
+// all of its heads, so no table of the context's length is kept.  The
 // rotation is fp32 with every product and sum rounded (no contraction), so
 // the same inputs give the same bits in the separate and the fused kernel.
 //
@@ -69,6 +69,28 @@ struct RopeParams {
     int inverse;
 };
 
+// sin and cos of 2 pi t, |t| <= 1/2, in fp64: t = q / 4 + r with |r| <= 1/8, the
+// Taylor series of x = 2 pi r to x^13 and x^14 (the next terms are below 2^-45),
+// and the quarter turns.  Rounded to fp32 this is the fp32 nearest the true
+// value but about once in 2^21.
+NVFP4_DEV void sincos_turns(double t, double& s, double& c) {
+    const double q = rint(4.0 * t);
+    const double x = (t - 0.25 * q) * 6.283185307179586476925, z = x * x;
+    double ps = 1.0 / 6227020800.0, pc = -1.0 / 87178291200.0;
+    ps = fma(ps, z, -1.0 / 39916800.0), pc = fma(pc, z, 1.0 / 479001600.0);
+    ps = fma(ps, z, 1.0 / 362880.0), pc = fma(pc, z, -1.0 / 3628800.0);
+    ps = fma(ps, z, -1.0 / 5040.0), pc = fma(pc, z, 1.0 / 40320.0);
+    ps = fma(ps, z, 1.0 / 120.0), pc = fma(pc, z, -1.0 / 720.0);
+    ps = fma(ps, z, -1.0 / 6.0), pc = fma(pc, z, 1.0 / 24.0);
+    pc = fma(pc, z, -0.5);
+    const double sn = fma(x * z, ps, x), cn = fma(pc, z, 1.0);
+    const int k = (int)q & 3;
+    s = (k & 1) ? cn : sn;
+    c = (k & 1) ? sn : cn;
+    if (k & 2) s = -s;
+    if (k == 1 || k == 2) c = -c;
+}
+
 // (cos, sin) of the CTA's tokens, ordered so that neighbouring lanes read
 // neighbouring words: pair p of token tl at [tl][p % w][p / w], w the pairs of a
 // run of 8 elements (8 where a run holds one element of each pair, else 4).
@@ -78,7 +100,7 @@ NVFP4_DEV void rope_angles(const RopeParams& rp, int64_t t0, int nt, float2* cs)
         const int tl = i / rp.pairs, p = i - tl * rp.pairs;
         const double turns = (double)rp.positions[t0 + tl] * rp.freqs[p];
         double s, c;
-        sincospi(2.0 * (turns - rint(turns)), &s, &c);
+        sincos_turns(turns - rint(turns), s, c);
         if (rp.inverse) s = -s;
         cs[tl * rp.pairs + (p & ((1 << lw) - 1)) * runs + (p >> lw)] =
             make_float2((float)(c * rp.mscale), (float)(s * rp.mscale));
@@ -124,8 +146,7 @@ NVFP4_DEV void rope_unit(const RopeParams& rp, int j, int tl, const float2* cs, 
 }
 
 constexpr int kCtaThreads = 256, kWarps = kCtaThreads / 32;
-constexpr int kBatch = 2;       // rows per lane whose loads go out together (reads of the cache: twice that)
-constexpr int kPasses = 4;      // rows per lane and head in a full CTA
+constexpr int kBatch = 2;       // rows per lane whose loads go out together
 constexpr int kMaxTokens = 32;  // tokens per CTA, at most
 
 // Units are as raw 16-byte words while they are on their way.
@@ -180,7 +201,7 @@ __global__ void __launch_bounds__(kCtaThreads, 4) rope_kernel(const XT* x, int64
     // lanes: `per` rows of `units` units (one row, 32 units at a time, for wide heads)
     const int lane = threadIdx.x & 31, per = units < 32 ? 32 / units : 1;
     const int row = units < 32 ? lane / units : 0, D = units * 16;
-    const int first = row < per ? row : kMaxTokens;  // lanes past the last row idle
+    const int first = row < per ? row : 0x40000000;  // lanes past the last row idle
     int j = lane - row * units, h = h0 + (threadIdx.x >> 5), tl0 = first, lo, hi;
     rope_runs(rp, j, D, lo, hi);
     Raw16<XT> raw[kBatch];
@@ -527,7 +548,7 @@ struct KvReadArgs {
 
 // Heads 0 .. heads - 1 are the keys, then the values.
 template <typename YT, int FMT, int D>
-__global__ void __launch_bounds__(kCtaThreads, 4) kv_read_kernel(const KvReadArgs a) {
+__global__ void __launch_bounds__(kCtaThreads, FMT == NVFP4_KV_BF16 ? 6 : 8) kv_read_kernel(const KvReadArgs a) {
     constexpr int units = D / 16, per = 32 / units;
     __shared__ Slot s_slot[kMaxTokens];
     griddep_launch_dependents();
@@ -551,7 +572,7 @@ __global__ void __launch_bounds__(kCtaThreads, 4) kv_read_kernel(const KvReadArg
         const uint8_t* base = a.c.data + hk * head_bytes;
         YT* out = (YT*)(is_v ? a.v_out : a.k_out) + t0 * y_ld + hk * D + j * 8;
         const float gs = is_v ? gv : gk;
-        constexpr int batch = FMT == NVFP4_KV_BF16 ? kBatch : 2 * kBatch;
+        constexpr int batch = kBatch;
         for (int tl0 = first; tl0 < nt; tl0 += batch * per) {
             RawRun<FMT> x[batch][2] = {};
 #pragma unroll
@@ -581,17 +602,21 @@ __global__ void __launch_bounds__(kCtaThreads, 4) kv_read_kernel(const KvReadArg
 // ---- launches ----------------------------------------------------------------
 
 // Tokens and heads of a CTA.  Where a warp per head and one pass of its lanes
-// leave the GPU unfilled (decode steps), that: latency counts.  Else four
-// passes, and as many heads as still leave about three CTAs per SM, so that
-// angles and slots are found once for all of them.
-static void cta_shape(int64_t T, int heads, int units, int& tt, int& hc) {
+// leave the GPU unfilled (decode steps), that: latency counts.  Else `passes`
+// passes, and as many heads as still leave `per_sm` CTAs per SM.  Rotations
+// take 4 and 4: angles are found once for more heads (8,191 x 40 heads, 64 of
+// 128 rotated: 29.9 us, against 32.1 with 16 per SM).  Plain writes and reads
+// take 2 and 16: nothing is shared but the slots, and short CTAs even out
+// better (10,240 tokens of 20 heads read after 2,048 are written, NVFP4: 35.0
+// us for both, against 37.4 with 4 passes).
+static void cta_shape(int64_t T, int heads, int units, int passes, int per_sm, int& tt, int& hc) {
     const int per = units < 32 ? 32 / units : 1;
     tt = per;
     hc = kWarps;
     if ((T + tt - 1) / tt * ((heads + hc - 1) / hc) > 148 * 4) {
-        tt = per * kPasses;
+        tt = per * passes;
         const int64_t groups = (T + tt - 1) / tt;
-        while (hc < heads && groups * ((heads + 2 * hc - 1) / (2 * hc)) >= 148 * 16) hc *= 2;
+        while (hc < heads && groups * ((heads + 2 * hc - 1) / (2 * hc)) >= 148 * per_sm) hc *= 2;
     }
 }
 
@@ -613,7 +638,7 @@ int launch_rope(const void* x, int x_dtype, int64_t T, int heads, int D, int64_t
                 int64_t y_ld, cudaStream_t st) {
     const RopeParams rp{positions, freqs, rot / 2, layout, mscale, inverse};
     int tt, hc;
-    cta_shape(T, heads, D / 16, tt, hc);
+    cta_shape(T, heads, D / 16, 4, 4, tt, hc);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, T, heads, tt, hc, (size_t)(tt * rp.pairs) * sizeof(float2), st);
     cudaError_t e;
@@ -658,7 +683,7 @@ int launch_kv_write(const KvView& c, const void* k, const void* v, int x_dtype, 
     a.T = T;
     a.slots = slots;
     a.status = status;
-    cta_shape(T, 2 * c.heads, c.head_dim / 16, a.tt, a.hc);
+    cta_shape(T, 2 * c.heads, c.head_dim / 16, 2, 16, a.tt, a.hc);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, T, 2 * c.heads, a.tt, a.hc, 0, st);
     const cudaError_t e = x_dtype == NVFP4_DTYPE_BF16 ? kv_write_fmt<__nv_bfloat16, false>(cfg, a)
@@ -685,7 +710,7 @@ int launch_rope_kv_write(const KvView& c, const void* q, const void* k, const vo
     a.q_out = (__nv_bfloat16*)q_out;
     a.status = status;
     const int heads = q_heads + 2 * c.heads;
-    cta_shape(T, heads, c.head_dim / 16, a.tt, a.hc);
+    cta_shape(T, heads, c.head_dim / 16, 4, 4, a.tt, a.hc);
     // angles; for NVFP4 a batch of bf16 key rows per warp
     const size_t rows = (size_t)kWarps * kBatch * (32 / (c.head_dim / 16)) * c.head_dim * 2;
     const size_t smem = (size_t)(a.tt * a.rp.pairs) * sizeof(float2) + (c.format == NVFP4_KV_NVFP4 ? rows : 0);
@@ -722,7 +747,7 @@ int launch_kv_read(const KvView& c, const int64_t* slots, int64_t T, void* k_out
     a.k_out = k_out;
     a.v_out = v_out;
     a.status = status;
-    cta_shape(T, 2 * c.heads, c.head_dim / 16, a.tt, a.hc);
+    cta_shape(T, 2 * c.heads, c.head_dim / 16, 2, 16, a.tt, a.hc);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, T, 2 * c.heads, a.tt, a.hc, 0, st);
     const cudaError_t e =

@@ -101,7 +101,8 @@ def test_bad_slots_are_reported_and_skipped(cuda_device):
                                    (torch.float32, torch.float32), (torch.bfloat16, torch.float32)])
 @pytest.mark.parametrize("T,heads,D,rot,start", [(1, 1, 16, 16, 5), (1, 60, 128, 128, 100003), (7, 3, 64, 32, 0),
                                                  (33, 5, 80, 48, 1 << 20), (2, 2, 256, 96, 1 << 31),
-                                                 (3, 2, 1024, 1024, 77), (700, 24, 128, 64, 4000)])
+                                                 (3, 2, 1024, 1024, 77), (700, 24, 128, 64, 4000),
+                                                 (2500, 20, 48, 32, 9), (900, 40, 80, 80, 70000), (3000, 9, 16, 16, 1)])
 def test_rope(cuda_device, T, heads, D, rot, start, xd, yd, interleaved):
     rng = np.random.default_rng([T, D, rot])
     x = rows(rng, T, heads, D, xd, extra=1) if D != 16 else dev(rng.standard_normal((T, heads, D))).to(xd)
