@@ -765,7 +765,8 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t T, 
     NVFP4_TRY(kv_view(cache, c));
     if (!slots || !k_out || !v_out) return NVFP4_ERR_NULL;
     if (!dtype_ok(y_dtype)) return NVFP4_ERR_DTYPE;
-    if (!rows_ok(T, (int64_t)c.heads * c.head_dim, (int64_t)c.heads * c.head_dim)) return NVFP4_ERR_SHAPE;
+    if (!rows_ok(T, (int64_t)c.heads * c.head_dim, (int64_t)c.heads * c.head_dim) || k_out == v_out)
+        return NVFP4_ERR_SHAPE;
     if (!aligned16(k_out) || !aligned16(v_out) || !aligned8(slots)) return NVFP4_ERR_ALIGN;
     NVFP4_TRY(check_arch());
     return launch_kv_read(c, slots, T, k_out, v_out, y_dtype, device_status_ptr(), (cudaStream_t)stream);
@@ -814,7 +815,7 @@ int nvfp4_attn_decode(const void* q, int64_t B, int32_t q_heads, int64_t q_ld, c
     if (!dtype_ok(y_dtype)) return NVFP4_ERR_DTYPE;
     const size_t need = attn_decode_workspace(c, B, q_heads, max_pages);
     if (!need || table_ld < max_pages || table_ld > ((int64_t)1 << 40) / B || window < 0 || !isfinite(scale) ||
-        !rows_ok(B, (int64_t)q_heads * c.head_dim, q_ld))
+        !rows_ok(B, (int64_t)q_heads * c.head_dim, q_ld) || y == q)
         return NVFP4_ERR_SHAPE;
     if (!aligned16(q) || !aligned16(y) || q_ld % 8 || ((uintptr_t)page_table & 3u) || ((uintptr_t)seq_lens & 3u) ||
         ((uintptr_t)lse & 3u))

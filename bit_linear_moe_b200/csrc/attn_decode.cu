@@ -22,8 +22,9 @@ static bool plan(const KvView& c, int64_t B, int q_heads, int64_t max_pages, Pla
     p.G = q_heads / c.heads;
     p.cols = cols_of(p.G, c.head_dim);
     p.chunks = (p.G + p.cols - 1) / p.cols;
-    // list positions are 32-bit: tiles and the cost of segments
-    if (max_pages > (int64_t)0x7fffffff / c.page_size) return false;
+    // tokens are int (a step may name 32 behind the last), list positions 32-bit:
+    // tiles and the cost of segments
+    if (max_pages > (int64_t)(0x7fffffff - 64) / c.page_size) return false;
     const int64_t seg = max_pages * (c.page_size / kKvTile) + kSegmentCost;
     if (seg > (int64_t)0x7fffffff / ((int64_t)c.heads * ((p.G + 7) / 8)) / B) return false;
     const int64_t tiles = B * max_pages * c.heads * p.chunks * (c.page_size / kKvTile);

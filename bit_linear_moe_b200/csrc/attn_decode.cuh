@@ -263,10 +263,10 @@ NVFP4_DEV float lse_of(float m, float l) {
 NVFP4_DEV float weight(float m, float M) { return m == __int_as_float(0xff800000) ? 0.0f : ex2(m - M); }
 
 // One tile's work for a warp.  YT only decides whether P keeps its low part:
-// with bf16 output P is rounded to fp16 once (2^-12 of each weight, random
-// in sign, against the 2^-9 of the output's own rounding); with fp32 output,
-// and for the bf16 cache (where P has to be bf16, 2^-9), P is split into a
-// high and a low part and multiplied twice.
+// with bf16 output P is rounded to fp16 once (at most 2^-11 of each weight,
+// random in sign, against the 2^-8 of the output's own rounding); with fp32
+// output, and for the bf16 cache (where P has to be bf16, 2^-8), P is split into
+// a high and a low part and multiplied twice.
 template <int FMT, int D, int NT, typename YT>
 struct Warp {
     using C = Cfg<FMT, D, NT>;

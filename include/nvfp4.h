@@ -504,8 +504,8 @@ int nvfp4_rope(const void* x, int x_dtype, int64_t T, int32_t heads, int32_t hea
  *   E4M3   E4M3 codes; value = E4M3(code) * gs       code = E4M3(x / gs), saturating
  *   NVFP4  value = E2M1(code) * E4M3(scale) * gs, the codes and block scales
  *          nvfp4_quantize gives each 16 elements with gs_in = gs
- * with one fp32 gs for the keys and one for the values (device; not read for
- * BF16).  `data` is [num_pages][heads][page_size / 16] tiles of 16 tokens, each
+ * with one fp32 gs for the keys and one for the values (device, positive and
+ * finite; not read for BF16).  `data` is [num_pages][heads][page_size / 16] tiles of 16 tokens, each
  * tile the 16 key rows, the 16 value rows (head_dim codes each, packed as
  * elsewhere), then for NVFP4 16 + 16 rows of head_dim / 16 scale bytes.  The
  * 16-byte pieces of the codes of a tile's row r (n of them) are permuted:
@@ -542,7 +542,7 @@ int nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k, const void* v, in
 
 /* nvfp4_kv_read:  the rows of slots[t], dequantized (fp32 product, rounded to
  * y_dtype), dense.
- *   k_out, v_out  [T, heads, head_dim] in y_dtype (F32 or BF16)
+ *   k_out, v_out  [T, heads, head_dim] in y_dtype (F32 or BF16), apart
  * A negative slot gives zeros; one out of range gives zeros and is reported as
  * NVFP4_ERR_PAGE.  A slot may be read more than once. */
 int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t T, void* k_out, void* v_out, int y_dtype,
@@ -590,8 +590,9 @@ int nvfp4_rope_kv_write(const nvfp4_kv_cache* cache, const void* q, const void* 
  * does not depend on anything but the arguments' shapes and values: the same
  * call gives the same bits.
  * Requires 1 <= B <= 4096, q_heads a multiple of cache->heads, max_pages >= 1,
- * B * heads * ceil(q_heads / heads / 8) * (max_pages * page_size / 16 + 2) and
- * max_pages * page_size below 2^31, q and y 16-byte aligned, q_ld % 8 == 0. */
+ * B * heads * ceil(q_heads / heads / 8) * (max_pages * page_size / 16 + 2) below
+ * 2^31, max_pages * page_size below 2^31 - 64, q and y 16-byte aligned,
+ * q_ld % 8 == 0, and y, lse and ws apart from each other and from all inputs. */
 size_t nvfp4_attn_decode_workspace(const nvfp4_kv_cache* cache, int64_t B, int32_t q_heads, int64_t max_pages);
 int nvfp4_attn_decode(const void* q, int64_t B, int32_t q_heads, int64_t q_ld, const nvfp4_kv_cache* cache,
                       const int32_t* page_table, int64_t max_pages, int64_t table_ld, const int32_t* seq_lens,

@@ -251,6 +251,30 @@ def test_large_batch(cuda_device, extra):
     b.check(y, lse, seqs=list(range(0, 1500, 37)) + [0, 255, 256, 511, 512, 1499])
 
 
+@pytest.mark.parametrize("D,fmt", [(64, oat.NVFP4), (256, oat.BF16)])
+@pytest.mark.parametrize("max_pages", [4, 1200])
+def test_largest_batch(cuda_device, D, fmt, max_pages):
+    """4,096 sequences that share their pages, 64 of each length 0 .. 63: every one is held to
+    the oracle's bound (the work split, and with it the rounding, differs between them)."""
+    one = Batch(fmt, D, 2, 2, 16, tuple(range(64)))
+    B = 4096
+    lens = torch.arange(B, device="cuda", dtype=torch.int32) % 64
+    table = torch.zeros((B, max_pages), dtype=torch.int32, device="cuda")
+    table[:, :4] = one.dtable[63, :4]
+    q = one.q[:1].expand(B, -1, -1).contiguous()
+    y, lse = nv.nvfp4_attn_decode(q, one.c, table, lens, want_lse=True)
+    for n in range(64):
+        k, v = one.rows(63, 0, n)
+        ry, rl, spread, mag = oat.attend(host(q[0]), k, v, D ** -0.5)
+        if n:
+            by, bl = attn_bounds(fmt, D, n, ry, rl, spread, mag, np.abs(v).max(), y.dtype)
+            for i in range(n, B, 64):
+                assert_close(y[i], ry, by, f"y, sequence {i}")
+                assert_close(lse[i], rl, bl, f"lse, sequence {i}")
+        else:
+            assert not y[::64].any() and (lse[::64] == -torch.inf).all()
+
+
 @WIDTHS
 def test_captured_graphs_share_a_workspace(cuda_device, extra):
     """Two captured calls with one workspace, replayed in turn on lengths that change on

@@ -199,6 +199,7 @@ def test_kv_validation(L):
         assert call(k=MISALIGNED) == nv.ERR_ALIGN and call(s=ctypes.c_void_p(0x10004)) == nv.ERR_ALIGN
         assert no_gpu(call)
     assert L.nvfp4_kv_write(None, FAKE, FAKE, 1, 1, 128, 128, FAKE, None) == nv.ERR_NULL
+    assert rd(v=FAKE) == nv.ERR_SHAPE                            # both outputs in one place
     assert w(xd=7) == nv.ERR_DTYPE and rd(yd=7) == nv.ERR_DTYPE and f(xd=7) == nv.ERR_DTYPE
     assert w(kl=127) == nv.ERR_SHAPE and w(vl=120) == nv.ERR_SHAPE and f(ql=248) == nv.ERR_SHAPE
     assert w(kl=132) == nv.ERR_ALIGN and no_gpu(w, kl=132, xd=nv.DTYPE_F32)
@@ -223,13 +224,19 @@ def test_attn_decode_validation(L):
         assert a_(**{n: None}) == nv.ERR_NULL
     assert a_(yd=4) == nv.ERR_DTYPE
     for kw in (dict(B=0), dict(B=4097, tl=5), dict(hq=7), dict(hq=0), dict(mp=0), dict(tl=4), dict(win=-1), dict(ql=504),
-               dict(sc=float("inf")), dict(sc=float("nan")), dict(mp=1 << 30, tl=1 << 30)):
+               dict(sc=float("inf")), dict(sc=float("nan")), dict(mp=1 << 30, tl=1 << 30),
+               dict(y=FAKE)):
         assert a_(**kw) == nv.ERR_SHAPE, kw
     for kw in (dict(q=MISALIGNED), dict(y=MISALIGNED), dict(ql=516), dict(t=ctypes.c_void_p(0x10002)),
                dict(sl=ctypes.c_void_p(0x10002)), dict(lse=ctypes.c_void_p(0x10002)), dict(ws=MISALIGNED)):
         assert a_(**kw) == nv.ERR_ALIGN, kw
     assert a_(ws=None) == nv.ERR_WORKSPACE and a_(wsb=64) == nv.ERR_WORKSPACE
-    assert no_gpu(a_) and no_gpu(a_, lse=FAKE3)
+    # the longest table: its tokens, and 32 behind them, are counted in 32 bits
+    long = ctypes.byref(desc(page_size=16, heads=1))
+    for pages, ok in (((1 << 27) - 1, False), ((1 << 27) - 4, False), ((1 << 27) - 5, True)):
+        kw = dict(B=1, hq=1, mp=pages, tl=pages)
+        assert no_gpu(a_, long, **kw) if ok else a_(long, **kw) == nv.ERR_SHAPE
+    assert no_gpu(a_) and no_gpu(a_, lse=FAKE3) and no_gpu(a_, B=4096, mp=40_000, tl=40_000)
 
 
 def test_python_refusals(L):
