@@ -767,7 +767,7 @@ def quantize_section(nv, torch, dev, reps=30):
 # ------------------------------------------------------------ profile cases ----
 
 CASES = ("decode_m1", "skinny_m4", "prefill_m2048", "quantize_m2048", "moe_t1", "moe_t32", "moe_t4096",
-         "moe_fused_t1", "moe_fused_t32", "stack_glue_m1")
+         "moe_fused_t1", "moe_fused_t32", "stack_glue_m1", "kv_attn_b8")
 
 
 def profile_case(args):
@@ -813,6 +813,28 @@ def profile_case(args):
 
         def run():
             nv.nvfp4_quantize(x, sf_layout=nv.SF_TILED)
+    elif case == "kv_attn_b8":
+        # the qkv rows of 2,048 tokens into the NVFP4 cache; then 8 sequences of 8,192 tokens (189 MB)
+        T, B, n, hq, hk, D, page = 2048, 8, 8192, 40, 20, 128, 64
+        gs = torch.full((1,), 0.01, device=dev)
+        cache = nv.KVCache.empty(B * n // page, page, hk, D, nv.KV_NVFP4, gs, gs, device=dev)
+        x = torch.randn((T, (hq + 2 * hk) * D), generator=gen, device=dev).to(torch.bfloat16)
+        q, k, v = (x[:, a * D:b * D].unflatten(1, (b - a, D)) for a, b in ((0, hq), (hq, hq + hk), (hq + hk, hq + 2 * hk)))
+        freqs = nv.nvfp4_rope_freqs(D)[0].to(dev)
+        slots = torch.arange(B * n, device=dev)
+        pos = slots % n
+        for t in range(0, B * n, T):
+            nv.nvfp4_kv_write(cache, k, v, slots[t:t + T])
+        table = torch.arange(B * n // page, dtype=torch.int32, device=dev).view(B, -1)
+        lens = torch.full((B,), n, dtype=torch.int32, device=dev)
+
+        def run():
+            nv.nvfp4_rope(q, pos[:T], freqs)
+            nv.nvfp4_kv_write(cache, k, v, slots[:T])
+            nv.nvfp4_kv_read(cache, slots[:8 * T])
+            nv.nvfp4_rope_kv_write(cache, q, k, v, pos[:T], slots[:T], freqs)
+            nv.nvfp4_attn_decode(q[:B], cache, table, lens)
+            nv.nvfp4_attn_decode(q[:1], cache, table[:1], lens[:1])
     else:
         E, H, I, k = synth.MOE_E, synth.MOE_H, synth.MOE_I, synth.MOE_K
         T = int(case.rsplit("_t", 1)[1])

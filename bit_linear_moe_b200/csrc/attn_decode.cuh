@@ -7,9 +7,9 @@
 //
 // Bound: HBM.  Each seen cache row is read once for all query heads of its
 // key head.  At G query heads per key head a cached byte (NVFP4, D = 128)
-// carries 4 * G / 1.125 flop, so the tensor cores are far from busy; what
-// has to be watched is the number of instructions per tile.  That is why the
-// products use warp-level mma (m16n8k16): the fragments come straight from the
+// carries 4 * G / 0.5625 / 2 flop, so the tensor cores are far from busy; what
+// has to be watched is the number of instructions per tile (355 a warp for an
+// NVFP4 tile at D = 128).  That is why the products use warp-level mma (m16n8k16): the fragments come straight from the
 // 4-bit codes in registers (no round trip of dequantized tiles through shared
 // or tensor memory), and N = 8 is the width that one token's query heads have.
 // Both products are taken transposed:
@@ -27,11 +27,29 @@
 // in cost: a segment counts kSegmentCost tiles more than it has, so that a
 // warp does not get a dozen one-tile segments.)  A
 // warp streams its tiles through a ring of its own (one bulk copy per tile,
-// S in flight) with its running maximum, sum and O^T in registers, and never
-// meets another warp until the end.  Segments that lie inside a warp are
-// written at once; the rest are joined per CTA through shared memory, and
+// a ring's worth in flight) with its running maximum, sum and O^T in registers,
+// and never meets another warp until the end.  Segments that lie inside a warp
+// are written at once; the rest are joined per CTA through shared memory, and
 // segments that span CTAs by attn_join_kernel from the workspace, in list
-// order (the same inputs give the same bits).
+// order (the same inputs give the same bits).  Few tiles per warp go to
+// attn_segment_kernel instead (kSegmentTiles).
+//
+// Measured (B200, replayed from a graph; floor: the bytes at 6,566 GB/s):
+//   32 ragged sequences of up to 16,384 tokens, 40 query / 20 key heads, NVFP4:
+//     169 us, 4.6 TB/s, 70 % of the floor.  Copies alone (no products) take 129;
+//     without the values' half 144, without the scores' 150 (of 190, then): what
+//     bounds it is issuing the conversions and fragments of both products.
+//   1 x 131,071, 32 / 8 heads, E4M3: 53 us, 5.1 TB/s, 78 %; copies alone 50
+//     (about 9 us of it before the first bytes and in the join).
+//   1 x 8,192, 40 / 20 heads, NVFP4: 13.2 us (segment kernel), latency: 8 tiles
+//     one after the other per warp, launch, page table and two joins.
+//   64 ragged x 2,048, 32 / 2 heads of 64, BF16: 14.5 us; 16 x 4,000 with a
+//     window of 1,000, 16 / 8 heads of 256, NVFP4: 13.5 us; 1 x 97: 4.2 us.
+// Slower, measured on the first of these: the scores on the block-scaled
+// tcgen05 MMA, queries as six NVFP4 terms (344 us; 382 with separate roles: a
+// tile's 16 rows fill an eighth of an MMA), codes unpacked by bit operations (217
+// against 191: a conversion takes a pair and names its byte), 10 warps per CTA
+// (210 against 191: the registers no longer hold a step of two tiles).
 #pragma once
 
 #include <atomic>
@@ -71,7 +89,12 @@ struct Args {
 struct Shape {
     int64_t grid, seg_tiles;
 };
-// Up to this many tiles per warp a cluster per segment is used.
+// Up to this many tiles per warp a cluster per segment is used.  Measured (us,
+// cluster per segment / even split): NVFP4, 20 key heads: 1 x 8,192 tokens (8 tiles
+// per warp) 13.3 / 16.4, 16 x 1,024 (8) 12.1 / 18.9, 1 x 16,384 (16) 21.6 / 22.1,
+// 16 x 4,096 (32) 36.1 / 35.4, 1 x 32,768 (32) 38.5 / 32.3; E4M3, 8 heads: 1 x 8,192
+// (8) 9.0 / 13.4, 4 x 16,384 (16) 20.1 / 24.4; BF16, 8 heads of 64: 1 x 16,384 (16)
+// 11.5 / 14.8.
 constexpr int64_t kSegmentTiles = 16;
 // What beginning and ending a segment costs a warp, in tiles (measured: 2 x
 // the 2,000 cycles of an NVFP4 tile at D = 128).
@@ -102,9 +125,9 @@ struct Cfg {
     static constexpr int kPieceBytes = Piece<D, NT>::kFloats * 4;
     static constexpr int kFixed = kRingBytes + kWarps * kPieceBytes;  // then the prefix
     static constexpr int kMt = D / 16;                                 // 16-row tiles of O^T
-    // Tiles a warp works on at a time.  Two where the codes are converted
-    // (about 450 instructions a tile): their chains interleave and share the
-    // softmax's exchange and the loop.
+    // Tiles a warp works on at a time.  Two where the codes are converted: their
+    // chains interleave and share the softmax's exchange and the loop (355
+    // instructions a tile, 450 one at a time).
     static constexpr int kStep = FMT == NVFP4_KV_NVFP4 && kRing >= 4 ? 2 : 1;
     static_assert(kRing >= 2, "one tile in flight while one is used");
     static_assert(kRing * kTile >= kPieceBytes, "a warp's last piece goes into its ring");
