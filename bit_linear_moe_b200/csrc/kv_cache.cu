@@ -18,22 +18,23 @@
 // the same inputs give the same bits in the separate and the fused kernel.
 //
 // All three kernels move each byte once and are bound by HBM for long chunks
-// and by latency for decode steps.  A thread takes units of 16 elements (one
-// NVFP4 block) of a row, a row being one head of one token.  A warp takes one
-// head at a time and the CTA's tokens along it, its lanes covering 2 to 8 whole
-// rows, so that everything but a row's place is known per head; the loads of
-// two rows per lane go out together (four, with the registers they take: 38.8 and
-// 45.0 us for the first two cases below).  All
-// are programmatic dependents.
+// and by latency for decode steps.  A thread takes units of 16 elements (two
+// runs of 8) of a row, a row being one head of one token.  A warp takes one
+// head at a time, its lanes covering 2 to 8 whole rows, so that everything but
+// a row's place is known per head; the loads of two rows per lane go out together
+// (four, with the registers they take: 38.8 and 45.0 us for the first two cases
+// below, against 29.7 and 35.0 of two then).  fp32 products go two to an
+// instruction.  All are programmatic dependents.
 //
 // Measured (B200, replayed from a graph):
-//   rotation of 8,191 tokens x 40 heads of 128, 64 rotated, bf16: 29.8 us, 5.6 TB/s
-//     (86 % of a copy's rate); one token: 2.0 us, the launch
-//   2,048 tokens of 20 heads written to NVFP4 pages and 10,240 read back: 35.0 us,
-//     4.6 TB/s (70 %): the quotients' brackets when writing (issue), byte and
-//     4-byte accesses when reading
-//   rotation, write and read of 2,048 tokens, 32 / 8 heads, bf16: 16.9 us, 4.0 TB/s
-//     (60 %): two short kernels, each with its ramp; 32 decoding tokens: 5.5 us
+//   rotation of 8,191 tokens x 40 heads of 128, 64 rotated, bf16: 27.6 us, 6.1 TB/s
+//     (92 % of a copy's rate); one token: 1.9 us, the launch
+//   2,048 tokens of 20 heads written to NVFP4 pages and 10,240 read back: 33.1 us,
+//     4.9 TB/s (74 %).  The write is what is slow (11.7 us alone, 4.1 of it bytes):
+//     some 19 instructions an element and two waves of CTAs, each with the latency of
+//     its first loads
+//   rotation, write and read of 2,048 tokens, 32 / 8 heads, bf16: 14.8 us, 4.5 TB/s
+//     (69 %): two short kernels, each with its ramp; 32 decoding tokens: 5.6 us
 #include "internal.h"
 #include "kv_layout.cuh"
 #include "quotient.cuh"
@@ -69,6 +70,35 @@ NVFP4_DEV void store8(float* p, const float (&v)[8]) {
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// Two fp32 operations in one instruction, each rounded (never contracted).
+NVFP4_DEV uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+NVFP4_DEV void unpack2(uint64_t p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+NVFP4_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+NVFP4_DEV uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+NVFP4_DEV uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// v[i] * f
+NVFP4_DEV void scale8(const float (&v)[8], float f, float (&y)[8]) {
+    const uint64_t ff = pack2(f, f);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) unpack2(mul2(pack2(v[i], v[i + 1]), ff), y[i], y[i + 1]);
+}
+
 // ---- rotary ------------------------------------------------------------------
 
 struct RopeParams {
@@ -102,19 +132,22 @@ NVFP4_DEV void sincos_turns(double t, double& s, double& c) {
     if (k == 1 || k == 2) c = -c;
 }
 
-// (cos, sin) of the CTA's tokens, ordered so that neighbouring lanes read
-// neighbouring words: pair p of token tl at [tl][p % w][p / w], w the pairs of a
-// run of 8 elements (8 where a run holds one element of each pair, else 4).
-NVFP4_DEV void rope_angles(const RopeParams& rp, int64_t t0, int nt, float2* cs) {
-    const int lw = rp.layout == NVFP4_ROPE_HALF ? 3 : 2, runs = rp.pairs >> lw;
+// cos and sin of the CTA's tokens, two pairs to a word (c, c', s, s') and ordered
+// so that neighbouring lanes read neighbouring words: pairs 2 m and 2 m + 1 of token
+// tl at [tl][m % w][m / w], w the words a run of 8 elements needs (4 where it
+// holds one element of each pair, else 2).
+NVFP4_DEV void rope_angles(const RopeParams& rp, int64_t t0, int nt, float4* cs) {
+    const int lw = rp.layout == NVFP4_ROPE_HALF ? 2 : 1, runs = rp.pairs >> (lw + 1);
+    float* out = reinterpret_cast<float*>(cs);
     for (int i = threadIdx.x; i < nt * rp.pairs; i += blockDim.x) {
-        const int tl = i / rp.pairs, p = i - tl * rp.pairs;
+        const int tl = i / rp.pairs, p = i - tl * rp.pairs, m = p >> 1;
         const double turns = (double)rp.positions[t0 + tl] * rp.freqs[p];
         double s, c;
         sincos_turns(turns - rint(turns), s, c);
         if (rp.inverse) s = -s;
-        cs[tl * rp.pairs + (p & ((1 << lw) - 1)) * runs + (p >> lw)] =
-            make_float2((float)(c * rp.mscale), (float)(s * rp.mscale));
+        const int at = 4 * (tl * (rp.pairs >> 1) + (m & ((1 << lw) - 1)) * runs + (m >> lw)) + (p & 1);
+        out[at] = (float)(c * rp.mscale);
+        out[at + 2] = (float)(s * rp.mscale);
     }
 }
 
@@ -132,33 +165,33 @@ NVFP4_DEV void rope_runs(const RopeParams& rp, int j, int D, int& lo, int& hi) {
     }
 }
 
-NVFP4_DEV void rotate(float& a, float& b, float2 cs) {
-    const float x = a, y = b;
-    a = __fsub_rn(__fmul_rn(x, cs.x), __fmul_rn(y, cs.y));
-    b = __fadd_rn(__fmul_rn(y, cs.x), __fmul_rn(x, cs.y));
+// Pairs (a0, b0) and (a1, b1).
+NVFP4_DEV void rotate2(float& a0, float& a1, float& b0, float& b1, const float4& cs) {
+    const uint64_t x = pack2(a0, a1), y = pack2(b0, b1), c = pack2(cs.x, cs.y), s = pack2(cs.z, cs.w);
+    unpack2(sub2(mul2(x, c), mul2(y, s)), a0, a1);
+    unpack2(add2(mul2(y, c), mul2(x, s)), b0, b1);
 }
 
 // Rotates the two runs of unit j of token tl.
-NVFP4_DEV void rope_unit(const RopeParams& rp, int j, int tl, const float2* cs, float (&lo)[8], float (&hi)[8]) {
+NVFP4_DEV void rope_unit(const RopeParams& rp, int j, int tl, const float4* cs, float (&lo)[8], float (&hi)[8]) {
     const int n8 = rp.pairs >> 3;
     if (j >= n8) return;
-    cs += tl * rp.pairs + j;
+    cs += tl * (rp.pairs >> 1) + j;
     if (rp.layout == NVFP4_ROPE_HALF) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) rotate(lo[i], hi[i], cs[i * n8]);
+        for (int i = 0; i < 4; ++i) rotate2(lo[2 * i], lo[2 * i + 1], hi[2 * i], hi[2 * i + 1], cs[i * n8]);
     } else {
         const int runs = 2 * n8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            rotate(lo[2 * i], lo[2 * i + 1], cs[i * runs]);
-            rotate(hi[2 * i], hi[2 * i + 1], cs[i * runs + n8]);
+        for (int i = 0; i < 2; ++i) {
+            rotate2(lo[4 * i], lo[4 * i + 2], lo[4 * i + 1], lo[4 * i + 3], cs[i * runs]);
+            rotate2(hi[4 * i], hi[4 * i + 2], hi[4 * i + 1], hi[4 * i + 3], cs[i * runs + n8]);
         }
     }
 }
 
 constexpr int kCtaThreads = 256, kWarps = kCtaThreads / 32;
-constexpr int kBatch = 2;       // rows per lane whose loads go out together
-constexpr int kMaxTokens = 32;  // tokens per CTA, at most
+constexpr int kBatch = 2;  // rows per lane whose loads go out together
 
 // Units are as raw 16-byte words while they are on their way.
 template <typename T>
@@ -203,7 +236,7 @@ template <typename XT, typename YT>
 __global__ void __launch_bounds__(kCtaThreads, 4) rope_kernel(const XT* x, int64_t T, int heads, int units, int64_t x_ld,
                                                            RopeParams rp, YT* y, int64_t y_ld, int tt, int hc) {
     extern __shared__ __align__(16) uint8_t smem[];
-    float2* cs = reinterpret_cast<float2*>(smem);
+    float4* cs = reinterpret_cast<float4*>(smem);
     griddep_launch_dependents();
     griddep_wait();
     const int64_t t0 = (int64_t)blockIdx.x * tt;
@@ -253,13 +286,14 @@ __global__ void __launch_bounds__(kCtaThreads, 4) rope_kernel(const XT* x, int64
 
 // ---- cache writes ------------------------------------------------------------
 
-// Global scale of one of K / V with what its quotients need.
+// Global scale of one of K / V with what its quotients need: reciprocals
+// within 2^-22 (0: divide).
 struct GsPar {
     float gs, denom, inv_denom, inv_gs;
 };
-NVFP4_DEV GsPar gs_par(const float* p) {
+NVFP4_DEV GsPar gs_par(float gs) {
     GsPar g;
-    g.gs = *p;
+    g.gs = gs;
     g.denom = __fmul_rn(g.gs, 6.0f);
     g.inv_denom = rcp_safe(g.denom) ? rcp_approx(g.denom) : 0.0f;
     g.inv_gs = rcp_safe(g.gs) ? rcp_approx(g.gs) : 0.0f;
@@ -271,103 +305,124 @@ NVFP4_DEV uint32_t f32x2_to_e4m3(float a, float b) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
     return r;
 }
-// E4M3 codes of RN(a / gs), RN(b / gs): the reciprocal product's bracket
-// decides (as e4m3_of_quotient, with a sign), the division where it does not.
-NVFP4_DEV uint32_t e4m3x2_of_quotients(float a, float b, const GsPar& g) {
-    if (g.inv_gs != 0.0f) {
-        const float p = __fmul_rn(a, g.inv_gs), q = __fmul_rn(b, g.inv_gs);
-        const uint32_t lo = f32x2_to_e4m3(__fmul_rn(p, kBracketLo), __fmul_rn(q, kBracketLo));
-        if (lo == f32x2_to_e4m3(__fmul_rn(p, kBracketHi), __fmul_rn(q, kBracketHi))) return lo;
-    }
-    return f32x2_to_e4m3(__fdiv_rn(a, g.gs), __fdiv_rn(b, g.gs));
+NVFP4_DEV uint2 f32x8_to_e4m3(const float (&v)[8]) {
+    return make_uint2(f32x2_to_e4m3(v[0], v[1]) | (f32x2_to_e4m3(v[2], v[3]) << 16),
+                      f32x2_to_e4m3(v[4], v[5]) | (f32x2_to_e4m3(v[6], v[7]) << 16));
+}
+NVFP4_DEV void divide8(const float (&v)[8], float r, float (&q)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], r);
 }
 
-// Where a token's rows lie: bytes from a head's first tile to its tile's codes
-// (key rows; -1: not stored), the tile row, and how its pieces are turned.
+// Codes of the quotients RN(v[i] / r), r > 0, of two runs x and y of a lane, without
+// dividing where that is certain: inv is within 2^-22 of 1 / r, so
+// v * RN(inv (1 - 2^-18)) and v * RN(inv (1 + 2^-18)), two roundings each, lie below
+// and above RN(v / r) in magnitude; rounding to a code is monotone, so where both
+// give one code it is that of RN(v / r).  (Products too small or too large
+// for that bound round to 0 or to the largest code either way.)  All is decided
+// first, without branches; one rare branch divides where that is needed.
+
+NVFP4_DEV void e4m3_runs(const float (&x)[8], const float (&y)[8], const GsPar& g, uint2& cx, uint2& cy) {
+    const float down = __fmul_rn(g.inv_gs, kBracketLo), up = __fmul_rn(g.inv_gs, kBracketHi);
+    float t[8];
+    scale8(x, down, t);
+    cx = f32x8_to_e4m3(t);
+    scale8(y, down, t);
+    cy = f32x8_to_e4m3(t);
+    scale8(x, up, t);
+    const uint2 dx = f32x8_to_e4m3(t);
+    scale8(y, up, t);
+    const uint2 dy = f32x8_to_e4m3(t);
+    if (((cx.x ^ dx.x) | (cx.y ^ dx.y) | (cy.x ^ dy.x) | (cy.y ^ dy.y)) != 0u || g.inv_gs == 0.0f) {
+        divide8(x, g.gs, t);
+        cx = f32x8_to_e4m3(t);
+        divide8(y, g.gs, t);
+        cy = f32x8_to_e4m3(t);
+    }
+}
+
+// NVFP4: also the block scale's E4M3 byte, of the block's amax (as
+// e4m3_of_quotient gives it).  diff: bits set in the codes that a division has to
+// decide; redo: so has the scale.
+struct Block {
+    uint32_t sb, code, diff;
+    float r;
+    bool redo;
+};
+NVFP4_DEV Block quick_block(const float (&v)[8], float amax, const GsPar& g) {
+    Block b;
+    const float a = __fmul_rn(amax, g.inv_denom);
+    const uint32_t pr = f32x2_to_e4m3(__fmul_rn(a, kBracketLo), __fmul_rn(a, kBracketHi));
+    b.sb = pr & 0xFFu;
+    b.r = __fmul_rn(e4m3_to_f32(b.sb), g.gs);
+    const bool safe = rcp_safe(b.r);
+    const float inv = safe ? rcp_approx(b.r) : 0.0f;
+    float t[8];
+    scale8(v, __fmul_rn(inv, kBracketLo), t);
+    b.code = f32x8_to_e2m1(t);
+    scale8(v, __fmul_rn(inv, kBracketHi), t);
+    b.diff = f32x8_to_e2m1(t) ^ b.code;
+    if (b.r == 0.0f) b.code = 0u;
+    b.redo = b.sb != pr >> 8 || g.inv_denom == 0.0f || !(safe || b.r == 0.0f);
+    return b;
+}
+NVFP4_DEV void mend_block(const float (&v)[8], float amax, const GsPar& g, Block& b) {
+    if (b.redo) {
+        b.sb = e4m3_of_quotient(amax, g.denom, 0.0f);
+        b.r = __fmul_rn(e4m3_to_f32(b.sb), g.gs);
+        b.code = 0u;
+        b.diff = b.r != 0.0f ? 0xFFFFFFFFu : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (b.diff & (0xFu << (4 * j)))
+            b.code = (b.code & ~(0xFu << (4 * j))) | (e2m1_of_division(v[j], b.r) << (4 * j));
+}
+
+// Where a token's rows lie, for head 0: the key row's codes `off` bytes from the
+// cache's start (-1: not stored), its block scales `scale` bytes on; its 16-byte
+// pieces are turned by `turn` bytes.  Values lie 16 rows further.
 struct Slot {
-    int64_t tile;
-    int r, turn;
+    int64_t off;
+    int scale, turn;
 };
 template <int FMT, int D>
 NVFP4_DEV void find_slots(const KvView& c, const int64_t* slots, int64_t t0, int nt, int64_t head_bytes, int* status,
                           Slot* out) {
+    constexpr int CB = kv_code_bytes(FMT, D);
     if ((int)threadIdx.x >= nt) return;
     const int64_t slot = slots[t0 + threadIdx.x];
     Slot s{-1, 0, 0};
     if (slot >= 0) {
         // (a 32-bit division where it does, which is nearly always)
         const int64_t page = slot >> 31 ? slot / c.page_size : (int64_t)((uint32_t)slot / (uint32_t)c.page_size);
-        const int in = (int)(slot - page * c.page_size);
-        s.r = in % kKvTile;
-        s.turn = kv_turn(s.r, kv_code_bytes(FMT, D) / 16);
+        const int in = (int)(slot - page * c.page_size), r = in % kKvTile;
+        s.scale = 2 * kKvTile * CB + r * (kv_scale_bytes(FMT, D) - CB);
+        s.turn = kv_turn(r, CB / 16) << 4;
         if (page < c.num_pages)
-            s.tile = page * c.heads * head_bytes + (int64_t)(in / kKvTile) * kv_tile_bytes(FMT, D);
+            s.off = page * c.heads * head_bytes + (int64_t)(in / kKvTile) * kv_tile_bytes(FMT, D) + r * CB;
         else if (status)
             atomicExch(status, NVFP4_ERR_PAGE);
     }
     out[threadIdx.x] = s;
 }
-
-// Address of byte o of row s.r of the keys (which 0) or values (1) of a tile.
+// Byte `o` of a row's codes (o: of element e, e * CB / D).
+NVFP4_DEV int turned(const Slot& s, int o) { return o ^ s.turn; }
+// From a key's code / scale bytes to its value's.
 template <int FMT, int D>
-NVFP4_DEV uint8_t* row_at(uint8_t* tile, int which, const Slot& s, int o) {
-    return tile + (which * kKvTile + s.r) * kv_code_bytes(FMT, D) + ((((o >> 4) ^ s.turn) << 4) | (o & 15));
+NVFP4_DEV constexpr int64_t value_codes() {
+    return kKvTile * kv_code_bytes(FMT, D);
 }
-template <int D>
-NVFP4_DEV uint8_t* scale_at(uint8_t* tile, int which, const Slot& s, int j) {
-    return tile + 2 * kKvTile * kv_code_bytes(NVFP4_KV_NVFP4, D) + (which * kKvTile + s.r) * (D / 16) + j;
-}
-
-// E2M1 codes (a word) of v[j] / r, j < 8: e2m1x16_of_quotients' argument for
-// half a block (amax: the block's).
-NVFP4_DEV uint32_t e2m1x8_of_quotients(const float (&v)[8], float amax, float r) {
-    const float inv = rcp_safe(r) ? rcp_approx(r) : 0.0f;
-    uint32_t code = 0u, diff = 0xFFFFFFFFu;
-    if (inv != 0.0f && __fmul_rn(amax, inv) < 15.0f) {
-        float lo[8], hi[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float p = __fmul_rn(v[j], inv);
-            lo[j] = __fmul_rn(p, kBracketLo);
-            hi[j] = __fmul_rn(p, kBracketHi);
-        }
-        code = f32x8_to_e2m1(hi);
-        diff = f32x8_to_e2m1(lo) ^ code;
-    }
-    if (diff) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (diff & (0xFu << (4 * j))) code = (code & ~(0xFu << (4 * j))) | (e2m1_of_division(v[j], r) << (4 * j));
-    }
-    return code;
-}
-
-// Eight elements e .. e + 7 of a row.  NVFP4: lanes 2 i and 2 i + 1 hold the
-// halves of a block; every lane of the warp calls (live: something is stored).
 template <int FMT, int D>
-NVFP4_DEV void store_run(bool live, uint8_t* tile, int which, const Slot& s, int e, const float (&v)[8],
-                         const GsPar& g) {
-    if constexpr (FMT == NVFP4_KV_BF16) {
-        if (live) *reinterpret_cast<uint4*>(row_at<FMT, D>(tile, which, s, 2 * e)) = pack8_bf16(v);
-    } else if constexpr (FMT == NVFP4_KV_E4M3) {
-        if (live) {
-            const uint32_t w0 = e4m3x2_of_quotients(v[0], v[1], g) | (e4m3x2_of_quotients(v[2], v[3], g) << 16);
-            const uint32_t w1 = e4m3x2_of_quotients(v[4], v[5], g) | (e4m3x2_of_quotients(v[6], v[7], g) << 16);
-            *reinterpret_cast<uint2*>(row_at<FMT, D>(tile, which, s, e)) = make_uint2(w0, w1);
-        }
-    } else {
-        float amax = 0.0f;
+NVFP4_DEV constexpr int value_scales() {
+    return kKvTile * (kv_scale_bytes(FMT, D) - kv_code_bytes(FMT, D));
+}
+
+NVFP4_DEV float amax8(const float (&v)[8]) {
+    float m = fabsf(v[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        if (live) {
-            const uint32_t sb = e4m3_of_quotient(amax, g.denom, g.inv_denom);
-            const float rsc = __fmul_rn(e4m3_to_f32(sb), g.gs);
-            *reinterpret_cast<uint32_t*>(row_at<FMT, D>(tile, which, s, e / 2)) =
-                rsc != 0.0f ? e2m1x8_of_quotients(v, amax, rsc) : 0u;
-            if ((e & 8) == 0) *scale_at<D>(tile, which, s, e / 16) = (uint8_t)sb;
-        }
-    }
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    return m;
 }
 
 struct KvWriteArgs {
@@ -379,21 +434,21 @@ struct KvWriteArgs {
     int64_t T;
     int q_heads;  // 0 without ROPE
     const int64_t* slots;
-    RopeParams rp;
+    RopeParams rp;         // without ROPE: head_dim / 2 pairs (the units' two runs)
     __nv_bfloat16* q_out;  // [T, q_heads, D]
-    int tt, hc;
+    int tt, hc;            // tt <= kBatch rows of lanes
     int* status;
 };
 
-// Heads 0 .. q_heads - 1 are the queries, then the keys, then the values.
-// Rotated keys of the NVFP4 cache pass through the warp's own piece of shared
-// memory (bf16): a unit's two runs of 8 lie in two blocks.
+// Heads 0 .. q_heads - 1 are the queries, then the keys, then the values.  An
+// NVFP4 block is two runs: those
+// of lanes 2 i and 2 i + 1, or, where the rotated part is an odd number of
+// units, of whichever lanes have runs 2 b and 2 b + 1 of the row.
 template <typename XT, int FMT, int D, bool ROPE>
 __global__ void __launch_bounds__(kCtaThreads, sizeof(XT) == 2 ? 4 : 3) kv_write_kernel(const KvWriteArgs a) {
-    constexpr int units = D / 16, per = 32 / units;
-    constexpr int batch = kBatch;
+    constexpr int units = D / 16, per = 32 / units, CB = kv_code_bytes(FMT, D);
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ Slot s_slot[kMaxTokens];
+    __shared__ Slot s_slot[kBatch * per];
     griddep_launch_dependents();
     griddep_wait();
     const int64_t t0 = (int64_t)blockIdx.x * a.tt;
@@ -402,118 +457,144 @@ __global__ void __launch_bounds__(kCtaThreads, sizeof(XT) == 2 ? 4 : 3) kv_write
     const int h0 = blockIdx.y * a.hc, h1 = min(heads, h0 + a.hc);
     const int64_t head_bytes = (int64_t)(a.c.page_size / kKvTile) * kv_tile_bytes(FMT, D);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % units, first = lane / units;
-    int h = h0 + warp, tb = 0;
-    Raw16<XT> raw[batch];
-    auto head_of = [&](int hh) { return hh < k0 ? hh : hh >= v0 ? hh - v0 : hh - k0; };
-    auto load = [&]() {  // the lane's rows of head h from token tb on
-        if (h >= h1) return;
-        const bool is_q = h < k0, is_v = h >= v0;  // without ROPE there are no queries
+    int lo, hi;
+    rope_runs(a.rp, j, D, lo, hi);
+    Raw16<XT> raw[kBatch];
+    auto load = [&](int h, int k) {  // the lane's row k of head h
+        if (h >= h1 || first + k * per >= nt) return;
+        const bool is_q = ROPE && h < k0, is_v = h >= v0;
         const int64_t ld = is_q ? a.q_ld : is_v ? a.v_ld : a.k_ld;
-        const XT* src = (is_q ? (const XT*)a.q : is_v ? (const XT*)a.v : (const XT*)a.k) + (t0 + tb + first) * ld +
-                        head_of(h) * D;
-        int lo = 8 * j, hi = D / 2 + 8 * j;
-        if (ROPE && !is_v) rope_runs(a.rp, j, D, lo, hi);
-#pragma unroll
-        for (int k = 0; k < batch; ++k)
-            if (tb + first + k * per < nt) raw[k].load(src + k * per * ld + lo, src + k * per * ld + hi);
+        const XT* src = (is_q ? (const XT*)a.q : is_v ? (const XT*)a.v : (const XT*)a.k) +
+                        (t0 + first + k * per) * ld + (is_q ? h : is_v ? h - v0 : h - k0) * D;
+        raw[k].load(src + lo, src + hi);
     };
 #pragma unroll
-    for (int k = 0; k < batch; ++k) raw[k].clear();
-    load();  // on their way while slots and angles are found
-    find_slots<FMT, D>(a.c, a.slots, t0, nt, head_bytes, a.status, s_slot);
-    float2* cs = reinterpret_cast<float2*>(smem);
-    if constexpr (ROPE) rope_angles(a.rp, t0, nt, cs);
-    GsPar gk{}, gv{};
-    if constexpr (FMT != NVFP4_KV_BF16) {
-        gk = gs_par(a.c.k_gs);
-        gv = gs_par(a.c.v_gs);
+    for (int k = 0; k < kBatch; ++k) {
+        raw[k].clear();
+        load(h0 + warp, k);  // on their way while slots and angles are found
     }
-    __nv_bfloat16* staged =
-        reinterpret_cast<__nv_bfloat16*>(smem + (ROPE ? a.tt * a.rp.pairs * (int)sizeof(float2) : 0)) +
-        warp * batch * per * D;
+    find_slots<FMT, D>(a.c, a.slots, t0, nt, head_bytes, a.status, s_slot);
+    const float4* cs = reinterpret_cast<const float4*>(smem);
+    if constexpr (ROPE) rope_angles(a.rp, t0, nt, reinterpret_cast<float4*>(smem));
+    float gk = 1.0f, gv = 1.0f;
+    if constexpr (FMT != NVFP4_KV_BF16) {
+        gk = *a.c.k_gs;
+        gv = *a.c.v_gs;
+    }
+    // the lane of the other half of each run's block, and whether it is that lane's hi
+    const int n8 = a.rp.pairs >> 3;
+    const bool paired = !ROPE || n8 % 2 == 0;
+    int lane_lo = 0, lane_hi = 0;
+    bool lo_hi = false, hi_hi = false;
+    if (FMT == NVFP4_KV_NVFP4 && !paired) {
+        auto find = [&](int run, int& ln, bool& in_hi) {
+            if (run < 2 * n8) {
+                in_hi = run >= n8;
+                ln = run - (in_hi ? n8 : 0);
+            } else {
+                in_hi = run - 2 * n8 >= units - n8;
+                ln = run - n8 - (in_hi ? units - n8 : 0);
+            }
+            ln += lane - j;
+        };
+        find((lo >> 3) ^ 1, lane_lo, lo_hi);
+        find((hi >> 3) ^ 1, lane_hi, hi_hi);
+    }
     __syncthreads();
-    while (h < h1) {
-        uint8_t* base = a.c.data + head_of(h) * head_bytes;
-        const bool is_q = h < k0, is_v = h >= v0, turned = ROPE && !is_v;
+    for (int h = h0 + warp; h < h1; h += kWarps) {
+        const bool is_q = ROPE && h < k0, is_v = h >= v0;
+        const int64_t at = (is_v ? h - v0 : h - k0) * head_bytes + (is_v ? value_codes<FMT, D>() : 0);
+        const int to_scales = is_v ? value_scales<FMT, D>() : 0;
+        const GsPar g = gs_par(is_v ? gv : gk);
 #pragma unroll
-        for (int k = 0; k < batch; ++k) {
-            const int tl = tb + first + k * per;
-            const bool in = tl < nt;
-            const Slot s = s_slot[in ? tl : 0];
-            const bool live = in && s.tile >= 0;
+        for (int k = 0; k < kBatch; ++k) {
+            const int tl = first + k * per;
             float x[8], y[8];
             raw[k].values(x, y);
-            if (ROPE && turned) {
-                int lo, hi;
-                rope_runs(a.rp, j, D, lo, hi);
-                if (in) rope_unit(a.rp, j, tl, cs, x, y);
+            if (ROPE) load(h + kWarps, k);  // on its way while this one is turned and quantized
+            if (ROPE && !is_v) {
+                if (tl < nt) rope_unit(a.rp, j, tl, cs, x, y);
+                const uint4 xw = pack8_bf16(x), yw = pack8_bf16(y);
                 if (is_q) {
-                    if (in) {
+                    if (tl < nt) {
                         __nv_bfloat16* yp = a.q_out + ((t0 + tl) * a.q_heads + h) * D;
-                        store8(yp + lo, x);
-                        store8(yp + hi, y);
+                        *reinterpret_cast<uint4*>(yp + lo) = xw;
+                        *reinterpret_cast<uint4*>(yp + hi) = yw;
                     }
-                } else if constexpr (FMT == NVFP4_KV_NVFP4) {
-                    store8(staged + (first + k * per) * D + lo, x);
-                    store8(staged + (first + k * per) * D + hi, y);
-                } else {  // quantized from the bf16 values
-                    const uint4 xw = pack8_bf16(x), yw = pack8_bf16(y);
-                    load8(reinterpret_cast<const __nv_bfloat16*>(&xw), x);
-                    load8(reinterpret_cast<const __nv_bfloat16*>(&yw), y);
-                    store_run<FMT, D>(live, base + s.tile, 0, s, lo, x, gk);
-                    store_run<FMT, D>(live, base + s.tile, 0, s, hi, y, gk);
+                    continue;
+                }
+                load8(reinterpret_cast<const __nv_bfloat16*>(&xw), x);  // quantized from the bf16 values
+                load8(reinterpret_cast<const __nv_bfloat16*>(&yw), y);
+            }
+            const Slot w = s_slot[tl < nt ? tl : 0];
+            const bool live = tl < nt && w.off >= 0;
+            uint8_t* codes = a.c.data + at + w.off;
+            uint8_t *p = codes + turned(w, lo * CB / D), *p_hi = codes + turned(w, hi * CB / D);
+            if constexpr (FMT == NVFP4_KV_BF16) {
+                if (live) {
+                    *reinterpret_cast<uint4*>(p) = pack8_bf16(x);
+                    *reinterpret_cast<uint4*>(p_hi) = pack8_bf16(y);
+                }
+            } else if constexpr (FMT == NVFP4_KV_E4M3) {
+                uint2 cx, cy;
+                e4m3_runs(x, y, g, cx, cy);
+                if (live) {
+                    *reinterpret_cast<uint2*>(p) = cx;
+                    *reinterpret_cast<uint2*>(p_hi) = cy;
                 }
             } else {
-                store_run<FMT, D>(live, base + s.tile, is_v, s, 8 * j, x, is_v ? gv : gk);
-                store_run<FMT, D>(live, base + s.tile, is_v, s, D / 2 + 8 * j, y, is_v ? gv : gk);
-            }
-        }
-        if constexpr (ROPE && FMT == NVFP4_KV_NVFP4) {
-            if (!is_q && !is_v) {
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < batch; ++k) {
-                    const int tl = tb + first + k * per;
-                    const Slot s = s_slot[tl < nt ? tl : 0];
-                    const bool live = tl < nt && s.tile >= 0;
-                    float x[8], y[8];
-                    load8(staged + (first + k * per) * D + 8 * j, x);
-                    load8(staged + (first + k * per) * D + D / 2 + 8 * j, y);
-                    store_run<FMT, D>(live, base + s.tile, 0, s, 8 * j, x, gk);
-                    store_run<FMT, D>(live, base + s.tile, 0, s, D / 2 + 8 * j, y, gk);
+                const float mx = amax8(x), my = amax8(y);
+                float ox, oy;
+                if (paired) {
+                    ox = __shfl_xor_sync(0xffffffffu, mx, 1);
+                    oy = __shfl_xor_sync(0xffffffffu, my, 1);
+                } else {
+                    const float b0 = __shfl_sync(0xffffffffu, mx, lane_lo), b1 = __shfl_sync(0xffffffffu, my, lane_lo);
+                    const float b2 = __shfl_sync(0xffffffffu, mx, lane_hi), b3 = __shfl_sync(0xffffffffu, my, lane_hi);
+                    ox = lo_hi ? b1 : b0;
+                    oy = hi_hi ? b3 : b2;
                 }
-                __syncwarp();
+                const float ax = fmaxf(mx, ox), ay = fmaxf(my, oy);
+                Block bx = quick_block(x, ax, g), by = quick_block(y, ay, g);
+                if ((bx.diff | by.diff) != 0u || bx.redo || by.redo) {
+                    mend_block(x, ax, g, bx);
+                    mend_block(y, ay, g, by);
+                }
+                if (live) {
+                    uint8_t* scale = codes + w.scale + to_scales;
+                    *reinterpret_cast<uint32_t*>(p) = bx.code;
+                    *reinterpret_cast<uint32_t*>(p_hi) = by.code;
+                    if ((lo & 8) == 0) scale[lo / 16] = (uint8_t)bx.sb;
+                    if ((hi & 8) == 0) scale[hi / 16] = (uint8_t)by.sb;
+                }
             }
         }
-        tb += batch * per;
-        if (tb >= nt) {
-            tb = 0;
-            h += kWarps;
+        if (!ROPE) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) load(h + kWarps, k);
         }
-        load();
     }
 }
 
 // ---- cache reads -------------------------------------------------------------
 
-// Eight elements e .. e + 7 of a tile row as stored, and their fp32 values.
+// Eight elements as stored, and their fp32 values.
 template <int FMT>
 struct RawRun {
     uint32_t c[FMT == NVFP4_KV_BF16 ? 4 : FMT == NVFP4_KV_E4M3 ? 2 : 1];
     uint32_t sb;
 };
-template <int FMT, int D>
-NVFP4_DEV void load_run(const uint8_t* tile_, int which, const Slot& s, int e, RawRun<FMT>& x) {
-    uint8_t* tile = const_cast<uint8_t*>(tile_);
+template <int FMT>
+NVFP4_DEV void load_run(const uint8_t* codes, const uint8_t* scale, RawRun<FMT>& x) {
     if constexpr (FMT == NVFP4_KV_BF16) {
-        const uint4 c = *reinterpret_cast<const uint4*>(row_at<FMT, D>(tile, which, s, 2 * e));
+        const uint4 c = *reinterpret_cast<const uint4*>(codes);
         x.c[0] = c.x, x.c[1] = c.y, x.c[2] = c.z, x.c[3] = c.w;
     } else if constexpr (FMT == NVFP4_KV_E4M3) {
-        const uint2 c = *reinterpret_cast<const uint2*>(row_at<FMT, D>(tile, which, s, e));
+        const uint2 c = *reinterpret_cast<const uint2*>(codes);
         x.c[0] = c.x, x.c[1] = c.y;
     } else {
-        x.c[0] = *reinterpret_cast<const uint32_t*>(row_at<FMT, D>(tile, which, s, e / 2));
-        x.sb = *scale_at<D>(tile, which, s, e / 16);
+        x.c[0] = *reinterpret_cast<const uint32_t*>(codes);
+        x.sb = *scale;
     }
 }
 template <int FMT>
@@ -538,12 +619,14 @@ NVFP4_DEV void run_values(const RawRun<FMT>& x, float gs, float (&v)[8]) {
                 p[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
         }
+        float f[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 f = f16x2_to_f32x2(p[i]);
-            v[2 * i] = __fmul_rn(f.x, gs);
-            v[2 * i + 1] = __fmul_rn(f.y, gs);
+            const float2 t = f16x2_to_f32x2(p[i]);
+            f[2 * i] = t.x;
+            f[2 * i + 1] = t.y;
         }
+        scale8(f, gs, v);
     }
 }
 
@@ -553,79 +636,77 @@ struct KvReadArgs {
     int64_t T;
     void* k_out;  // [T, heads, D]
     void* v_out;
-    int tt, hc;
+    int tt, hc;  // as in KvWriteArgs
     int* status;
 };
 
 // Heads 0 .. heads - 1 are the keys, then the values.
 template <typename YT, int FMT, int D>
-__global__ void __launch_bounds__(kCtaThreads, FMT == NVFP4_KV_BF16 ? 6 : 8) kv_read_kernel(const KvReadArgs a) {
-    constexpr int units = D / 16, per = 32 / units;
-    __shared__ Slot s_slot[kMaxTokens];
+__global__ void __launch_bounds__(kCtaThreads, 6) kv_read_kernel(const KvReadArgs a) {
+    constexpr int units = D / 16, per = 32 / units, CB = kv_code_bytes(FMT, D);
+    __shared__ Slot s_slot[kBatch * per];
     griddep_launch_dependents();
     griddep_wait();
     const int64_t t0 = (int64_t)blockIdx.x * a.tt;
     const int nt = (int)(a.T - t0 < a.tt ? a.T - t0 : a.tt);
     const int h0 = blockIdx.y * a.hc, h1 = min(2 * a.c.heads, h0 + a.hc);
     const int64_t head_bytes = (int64_t)(a.c.page_size / kKvTile) * kv_tile_bytes(FMT, D);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % units, first = lane / units;
     find_slots<FMT, D>(a.c, a.slots, t0, nt, head_bytes, a.status, s_slot);
     float gk = 1.0f, gv = 1.0f;
     if constexpr (FMT != NVFP4_KV_BF16) {
         gk = *a.c.k_gs;
         gv = *a.c.v_gs;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % units, first = lane / units;
-    const int64_t y_ld = (int64_t)a.c.heads * D;
     __syncthreads();
+    const int64_t y_ld = (int64_t)a.c.heads * D, y_row = (t0 + first) * y_ld + 8 * j;
     for (int h = h0 + warp; h < h1; h += kWarps) {
         const bool is_v = h >= a.c.heads;
         const int hk = is_v ? h - a.c.heads : h;
-        const uint8_t* base = a.c.data + hk * head_bytes;
-        YT* out = (YT*)(is_v ? a.v_out : a.k_out) + t0 * y_ld + hk * D + j * 8;
-        const float gs = is_v ? gv : gk;
-        constexpr int batch = kBatch;
-        for (int tl0 = first; tl0 < nt; tl0 += batch * per) {
-            RawRun<FMT> x[batch][2] = {};
+        const int64_t at = hk * head_bytes + (is_v ? value_codes<FMT, D>() : 0);
+        const int to_scales = is_v ? value_scales<FMT, D>() : 0;
+        RawRun<FMT> x[kBatch][2] = {};
 #pragma unroll
-            for (int k = 0; k < batch; ++k) {
-                const int tl = tl0 + k * per;
-                const Slot s = s_slot[tl < nt ? tl : 0];
-                if (tl < nt && s.tile >= 0) {
-                    load_run<FMT, D>(base + s.tile, is_v, s, 8 * j, x[k][0]);
-                    load_run<FMT, D>(base + s.tile, is_v, s, D / 2 + 8 * j, x[k][1]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < batch; ++k) {
-                const int tl = tl0 + k * per;
-                if (tl < nt) {
-                    float v[8];
-                    run_values<FMT>(x[k][0], gs, v);
-                    store8(out + tl * y_ld, v);
-                    run_values<FMT>(x[k][1], gs, v);
-                    store8(out + tl * y_ld + D / 2, v);
-                }
+        for (int k = 0; k < kBatch; ++k) {
+            const int tl = first + k * per;
+            const Slot w = s_slot[tl < nt ? tl : 0];
+            if (tl < nt && w.off >= 0) {
+                const uint8_t* codes = a.c.data + at + w.off;
+                const uint8_t* scale = codes + w.scale + to_scales + j / 2;
+                load_run<FMT>(codes + turned(w, j * CB / units / 2), scale, x[k][0]);
+                load_run<FMT>(codes + turned(w, CB / 2 + j * CB / units / 2), scale + D / 32, x[k][1]);
             }
         }
+        YT* out = (YT*)(is_v ? a.v_out : a.k_out) + y_row + hk * D;
+        const float gs = is_v ? gv : gk;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (first + k * per < nt) {
+                float v[8];
+                run_values<FMT>(x[k][0], gs, v);
+                store8(out + k * per * y_ld, v);
+                run_values<FMT>(x[k][1], gs, v);
+                store8(out + k * per * y_ld + D / 2, v);
+            }
     }
 }
 
 // ---- launches ----------------------------------------------------------------
 
-// Tokens and heads of a CTA.  Where a warp per head and one pass of its lanes
-// leave the GPU unfilled (decode steps), that: latency counts.  Else `passes`
-// passes, and as many heads as still leave `per_sm` CTAs per SM.  Rotations
-// take 4 and 4: angles are found once for more heads (8,191 x 40 heads, 64 of
-// 128 rotated: 29.9 us, against 32.1 with 16 per SM).  Plain writes and reads
-// take 2 and 16: nothing is shared but the slots, and short CTAs even out
-// better (10,240 tokens of 20 heads read after 2,048 are written, NVFP4: 35.0
-// us for both, against 37.4 with 4 passes).
-static void cta_shape(int64_t T, int heads, int units, int passes, int per_sm, int& tt, int& hc) {
+// Tokens and heads of a CTA.  Where a warp per head and one row per lane leave
+// the GPU unfilled (decode steps), that: latency counts.  Else kBatch rows per lane,
+// and as many heads as still leave `per_sm` CTAs per SM: more heads share the
+// CTA's angles and slots, more CTAs even out better.  Measured (us): rotation of
+// 8,191 x 40 heads with 4 / 8 / 16 per SM 28.2 / 27.5 / 28.3 (four rows per lane, 4:
+// 28.8); rotation and write of 2,048 x (40 + 2 x 20) heads, NVFP4, with 4 / 8: 23.0 /
+// 24.6 (four rows, 4: 32.9), 32 + 2 x 8 heads, bf16: 11.3 / 12.8; write of 2,048 x 2 x
+// 20 heads, NVFP4, with 4 / 16: 11.7 / 12.5; read of them 6.1 / 5.5.
+static void cta_shape(int64_t T, int heads, int units, int per_sm, int& tt, int& hc) {
     const int per = units < 32 ? 32 / units : 1;
     tt = per;
     hc = kWarps;
     if ((T + tt - 1) / tt * ((heads + hc - 1) / hc) > 148 * 4) {
-        tt = per * passes;
+        tt = per * kBatch;
         const int64_t groups = (T + tt - 1) / tt;
         while (hc < heads && groups * ((heads + 2 * hc - 1) / (2 * hc)) >= 148 * per_sm) hc *= 2;
     }
@@ -649,7 +730,7 @@ int launch_rope(const void* x, int x_dtype, int64_t T, int heads, int D, int64_t
                 int64_t y_ld, cudaStream_t st) {
     const RopeParams rp{positions, freqs, rot / 2, layout, mscale, inverse};
     int tt, hc;
-    cta_shape(T, heads, D / 16, 4, 4, tt, hc);
+    cta_shape(T, heads, D / 16, 8, tt, hc);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, T, heads, tt, hc, (size_t)(tt * rp.pairs) * sizeof(float2), st);
     cudaError_t e;
@@ -693,8 +774,9 @@ int launch_kv_write(const KvView& c, const void* k, const void* v, int x_dtype, 
     a.v_ld = v_ld;
     a.T = T;
     a.slots = slots;
+    a.rp.pairs = c.head_dim / 2;
     a.status = status;
-    cta_shape(T, 2 * c.heads, c.head_dim / 16, 2, 16, a.tt, a.hc);
+    cta_shape(T, 2 * c.heads, c.head_dim / 16, 4, a.tt, a.hc);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, T, 2 * c.heads, a.tt, a.hc, 0, st);
     const cudaError_t e = x_dtype == NVFP4_DTYPE_BF16 ? kv_write_fmt<__nv_bfloat16, false>(cfg, a)
@@ -721,10 +803,8 @@ int launch_rope_kv_write(const KvView& c, const void* q, const void* k, const vo
     a.q_out = (__nv_bfloat16*)q_out;
     a.status = status;
     const int heads = q_heads + 2 * c.heads;
-    cta_shape(T, heads, c.head_dim / 16, 4, 4, a.tt, a.hc);
-    // angles; for NVFP4 a batch of bf16 key rows per warp
-    const size_t rows = (size_t)kWarps * kBatch * (32 / (c.head_dim / 16)) * c.head_dim * 2;
-    const size_t smem = (size_t)(a.tt * a.rp.pairs) * sizeof(float2) + (c.format == NVFP4_KV_NVFP4 ? rows : 0);
+    cta_shape(T, heads, c.head_dim / 16, 4, a.tt, a.hc);
+    const size_t smem = (size_t)(a.tt * a.rp.pairs) * sizeof(float2);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, T, heads, a.tt, a.hc, smem, st);
     const cudaError_t e = x_dtype == NVFP4_DTYPE_BF16 ? kv_write_fmt<__nv_bfloat16, true>(cfg, a)
@@ -758,7 +838,7 @@ int launch_kv_read(const KvView& c, const int64_t* slots, int64_t T, void* k_out
     a.k_out = k_out;
     a.v_out = v_out;
     a.status = status;
-    cta_shape(T, 2 * c.heads, c.head_dim / 16, 2, 16, a.tt, a.hc);
+    cta_shape(T, 2 * c.heads, c.head_dim / 16, 16, a.tt, a.hc);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, T, 2 * c.heads, a.tt, a.hc, 0, st);
     const cudaError_t e =
