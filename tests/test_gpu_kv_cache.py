@@ -80,6 +80,32 @@ def test_kv_write_large_chunk(cuda_device, fmt):
         assert torch.equal(y, ref)
 
 
+@pytest.mark.parametrize("fmt", [oat.E4M3, oat.NVFP4])
+@pytest.mark.parametrize("gs", [2.0 ** -140, 1.2e-38, 2.0 ** -20, 0.0123, 1.0, 1e30, 5e37])
+def test_kv_write_on_the_borders(cuda_device, fmt, gs):
+    """Quotients on and one step beside the borders between codes, of every block scale,
+    with global scales to the ends of fp32: bytes equal to those of the divisions."""
+    rng = np.random.default_rng(7)
+    T, heads, D, page = 64, 2, 64, 16
+    g = np.float32(gs)
+    oc = oat.Cache(T // page, page, heads, D, fmt, g, g)
+    c = device_cache(oc)
+    border = np.float32([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 0.5, 1.0, 2.0, 3.0, 4.0, 0.0, 17 / 16, 27 / 16])
+    with np.errstate(all="ignore"):
+        scale = np.float32(rng.integers(8, 16, (T, heads, D // 16, 1)) * 2.0 ** rng.integers(-4, 5, (T, heads, D // 16, 1)))
+        k = (border[rng.integers(0, 16, (T, heads, D // 16, 16))] * scale * g).astype(np.float32)
+        k[..., 0] = (np.float32(6.0) * scale * g)[..., 0]        # the block's largest names its scale
+        step = rng.integers(-1, 2, k.shape)
+        k = np.where(step < 0, np.nextafter(k, np.float32(0)), np.where(step > 0, np.nextafter(k, np.float32(np.inf)), k))
+        k = np.where(rng.random(k.shape) < 0.5, -k, k).astype(np.float32).reshape(T, heads, D)
+    k = np.clip(k, -3e38, 3e38)
+    v = np.ascontiguousarray(k[::-1])
+    nv.nvfp4_kv_write(c, dev(k), dev(v), torch.arange(T, device="cuda"))
+    with np.errstate(all="ignore"):
+        oc.write(k, v, np.arange(T))
+    assert np.array_equal(c.data.cpu().numpy(), oc.data)
+
+
 def test_bad_slots_are_reported_and_skipped(cuda_device):
     """Slots past the cache: skipped by the kernel's own check, named in the status word."""
     oc = oat.Cache(2, 16, 2, 64, oat.E4M3, 0.01, 0.01)
