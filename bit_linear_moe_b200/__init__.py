@@ -538,15 +538,19 @@ def nvfp4_kv_read(cache: KVCache, slots: torch.Tensor, k_out=None, v_out=None, y
     tensors (bf16 or fp32); zeros for negative slots."""
     dev = cache.device
     T, heads, D = slots.numel(), cache.heads, cache.head_dim
-    if k_out is None:
-        k_out = torch.empty(T, heads, D, dtype=y_dtype if v_out is None else v_out.dtype, device=dev)
-    if v_out is None:
-        v_out = torch.empty(T, heads, D, dtype=k_out.dtype, device=dev)
-    if k_out.dtype != v_out.dtype:
-        raise TypeError("k_out and v_out must have one dtype")
-    code, n = _dtype_code(k_out), T * heads * D
-    _launch(dev, "nvfp4_kv_read", (cache._ref, _vector(slots, torch.int64, T, dev, "slots"), T,
-            _vector(k_out, k_out.dtype, n, dev, "k_out"), _vector(v_out, v_out.dtype, n, dev, "v_out"), code))
+    if k_out is None and v_out is None:
+        k_out = torch.empty(T, heads, D, dtype=y_dtype, device=dev)
+        v_out = torch.empty_like(k_out)
+        k_ptr, v_ptr = k_out.data_ptr(), v_out.data_ptr()
+    else:
+        k_out = torch.empty(T, heads, D, dtype=v_out.dtype, device=dev) if k_out is None else k_out
+        v_out = torch.empty(T, heads, D, dtype=k_out.dtype, device=dev) if v_out is None else v_out
+        if k_out.dtype != v_out.dtype:
+            raise TypeError("k_out and v_out must have one dtype")
+        k_ptr = _vector(k_out, k_out.dtype, T * heads * D, dev, "k_out")
+        v_ptr = _vector(v_out, v_out.dtype, T * heads * D, dev, "v_out")
+    _launch(dev, "nvfp4_kv_read", (cache._ref, _vector(slots, torch.int64, T, dev, "slots"), T, k_ptr, v_ptr,
+            _dtype_code(k_out)))
     return k_out, v_out
 
 
@@ -594,7 +598,9 @@ def nvfp4_attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     table_ld = page_table.stride(0) if B > 1 else max_pages
     if y is None:
         y = torch.empty(B, q_heads, D, dtype=y_dtype, device=dev)
-    y_ptr = _vector(y, y.dtype, B * q_heads * D, dev, "y")
+        y_ptr = y.data_ptr()
+    else:
+        y_ptr = _vector(y, y.dtype, B * q_heads * D, dev, "y")
     lse = torch.empty((B, q_heads), dtype=torch.float32, device=dev) if want_lse else None
     if ws is None:
         ws = torch.empty(nvfp4_attn_decode_workspace(cache, B, q_heads, max_pages), dtype=torch.uint8, device=dev)

@@ -669,8 +669,9 @@ int nvfp4_rope_freqs(int32_t rot_dim, double theta, int scaling, double factor, 
                      double beta_slow, double* freqs, double* mscale_out) {
     if (!freqs || !mscale_out) return NVFP4_ERR_NULL;
     if (scaling < NVFP4_ROPE_SCALE_NONE || scaling > NVFP4_ROPE_SCALE_YARN) return NVFP4_ERR_MODE;
-    if (rot_dim < 2 || rot_dim > 1024 || rot_dim % 2 || !(theta > 0.0)) return NVFP4_ERR_SHAPE;
-    if (scaling != NVFP4_ROPE_SCALE_NONE && !(factor >= 1.0)) return NVFP4_ERR_SHAPE;
+    if (rot_dim < 2 || rot_dim > 1024 || rot_dim % 2 || !(theta > 0.0) || !isfinite(theta))
+        return NVFP4_ERR_SHAPE;
+    if (scaling != NVFP4_ROPE_SCALE_NONE && !(factor >= 1.0 && isfinite(factor))) return NVFP4_ERR_SHAPE;
     if (scaling == NVFP4_ROPE_SCALE_NTK && rot_dim < 4) return NVFP4_ERR_SHAPE;
     if (scaling == NVFP4_ROPE_SCALE_YARN && (!(original_len >= 1.0) || !(beta_fast > beta_slow)))
         return NVFP4_ERR_SHAPE;

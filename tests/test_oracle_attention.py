@@ -106,7 +106,8 @@ def test_rope_freqs_refusals(L):
                dict(rot_dim=32, theta=-1.0), dict(rot_dim=32, scaling=nv.ROPE_SCALE_LINEAR, factor=0.5),
                dict(rot_dim=32, scaling=nv.ROPE_SCALE_YARN, factor=2.0),
                dict(rot_dim=32, scaling=nv.ROPE_SCALE_YARN, factor=2.0, original_len=10.0, beta_fast=1.0),
-               dict(rot_dim=32, theta=float("nan"))):
+               dict(rot_dim=32, theta=float("nan")), dict(rot_dim=32, theta=float("inf")),
+               dict(rot_dim=32, scaling=nv.ROPE_SCALE_LINEAR, factor=float("inf"))):
         with pytest.raises(nv.NVFP4Error) as e:
             nv.nvfp4_rope_freqs(**kw)
         assert e.value.status == nv.ERR_SHAPE
