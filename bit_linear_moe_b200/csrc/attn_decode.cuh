@@ -90,11 +90,12 @@ struct Shape {
     int64_t grid, seg_tiles;
 };
 // Up to this many tiles per warp a cluster per segment is used.  Measured (us,
-// cluster per segment / even split): NVFP4, 20 key heads: 1 x 8,192 tokens (8 tiles
-// per warp) 13.3 / 16.4, 16 x 1,024 (8) 12.1 / 18.9, 1 x 16,384 (16) 21.6 / 22.1,
-// 16 x 4,096 (32) 36.1 / 35.4, 1 x 32,768 (32) 38.5 / 32.3; E4M3, 8 heads: 1 x 8,192
-// (8) 9.0 / 13.4, 4 x 16,384 (16) 20.1 / 24.4; BF16, 8 heads of 64: 1 x 16,384 (16)
-// 11.5 / 14.8.
+// cluster per segment / even split, and the cluster's tiles per warp): NVFP4, 20 key
+// heads of 128: 1 x 8,192 tokens (8) 13.2 / 16.4, 16 x 1,024 (8) 12.1 / 19.1, 1 x 16,384
+// (16) 21.8 / 21.9, 16 x 4,096 (32) 36.0 / 35.3, 1 x 32,768 (32) 38.4 / 32.5; 8 heads of
+// 256: 1 x 4,096 (8) 10.9 / 12.7, 1 x 8,192 (16) 16.1 / 15.0; E4M3, 8 heads of 128: 4 x
+// 16,384 (16) 19.9 / 24.4, 1 x 32,768 (32) 23.6 / 23.2; BF16, 8 heads of 128: 4 x 4,096
+// (8) 10.9 / 14.2, 1 x 16,384 (32) 24.5 / 22.5.
 constexpr int64_t kSegmentTiles = 16;
 // What beginning and ending a segment costs a warp, in tiles (measured: 2 x
 // the 2,000 cycles of an NVFP4 tile at D = 128).
