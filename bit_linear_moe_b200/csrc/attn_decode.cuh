@@ -1184,35 +1184,41 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const Args a) {
     const int step = kRows == 1 ? 8 : 1, off = kRows == 1 ? warp : 0;
     using Pc = Piece<D, NT>;
     auto part = [&](uint32_t c) { return a.partial + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * Pc::kFloats; };
-    // maximum over the pieces, lanes striding over them
-    float M = __int_as_float(0xff800000);
-    for (uint32_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c)[Pc::kMax + col]);
-    M = warp_max(M);
-    float v[kV], L = 0.0f;
+    // one pass with a running maximum, so that a piece's maximum, sum and values are
+    // on their way together
+    float M = __int_as_float(0xff800000), L = 0.0f, v[kV];
 #pragma unroll
     for (int k = 0; k < kV; ++k) v[k] = 0.0f;
+    auto add = [&](float m, float l, const float(&x)[kV]) {
+        const float top = fmaxf(M, m), wo = weight(M, top), wn = weight(m, top);
+        L = L * wo + wn * l;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) v[k] = v[k] * wo + wn * x[k];
+        M = top;
+    };
 #pragma unroll 4
     for (uint32_t c = c0 + off; c <= c1; c += step) {
         const float* src = part(c);
-        const float w = weight(src[Pc::kMax + col], M);
-        L += w * src[Pc::kSum + col];
+        float x[kV];
 #pragma unroll
-        for (int k = 0; k < kV; ++k) v[k] += w * src[col * Pc::kLd + lane + 32 * k];
+        for (int k = 0; k < kV; ++k) x[k] = src[col * Pc::kLd + lane + 32 * k];
+        add(src[Pc::kMax + col], src[Pc::kSum + col], x);
     }
     if constexpr (kRows == 1) {
-        __shared__ float s_v[8][D + 1];
+        __shared__ float s_v[8][D + 2];
 #pragma unroll
         for (int k = 0; k < kV; ++k) s_v[warp][lane + 32 * k] = v[k];
-        if (lane == 0) s_v[warp][D] = L;
+        if (lane == 0) {
+            s_v[warp][D] = M;
+            s_v[warp][D + 1] = L;
+        }
         __syncthreads();
         if (warp) return;
-        L = 0.0f;
+        for (int w = 1; w < 8; ++w) {
+            float x[kV];
 #pragma unroll
-        for (int k = 0; k < kV; ++k) v[k] = 0.0f;
-        for (int w = 0; w < 8; ++w) {
-            L += s_v[w][D];
-#pragma unroll
-            for (int k = 0; k < kV; ++k) v[k] += s_v[w][lane + 32 * k];
+            for (int k = 0; k < kV; ++k) x[k] = s_v[w][lane + 32 * k];
+            add(s_v[w][D], s_v[w][D + 1], x);
         }
     }
     const float inv = inverse_sum(L);
