@@ -376,6 +376,11 @@ struct Warp {
         sc[1] = prmt(h, h, 0x3232);
     }
 
+    // Would a score x weigh more than 2^8?  fp16 cannot hold 2^16, so the difference is
+    // rounded as the weight's exponent is: scores from 2^26 on lie 8 and more apart, and
+    // m + 8 may round to m + 16.
+    static NVFP4_DEV bool passes(float x, float m) { return kBf16 ? x > m + 8.0f : x - m > 8.0f; }
+
     // kStep tiles with tokens tok0 .. tok0 + 16 kStep - 1 at tp[0], tp[1]; tokens
     // outside [lo, hi) are masked (their bytes may be anything, NaN included).
     static constexpr int kStep = C::kStep;
@@ -411,7 +416,7 @@ struct Warp {
                 up[0] = fmaxf(up[0], fmaxf(x[1][0], x[1][2]));
                 up[1] = fmaxf(up[1], fmaxf(x[1][1], x[1][3]));
             }
-            if (__any_sync(0xffffffffu, up[0] > m[n][0] + 8.0f || up[1] > m[n][1] + 8.0f)) {
+            if (__any_sync(0xffffffffu, passes(up[0], m[n][0]) || passes(up[1], m[n][1]))) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     float mx = up[c];
