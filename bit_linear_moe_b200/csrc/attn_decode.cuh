@@ -286,16 +286,29 @@ NVFP4_DEV float lse_of(float m, float l) {
 // The weights of two pieces' running maxima.
 NVFP4_DEV float weight(float m, float M) { return m == __int_as_float(0xff800000) ? 0.0f : ex2(m - M); }
 
-// One tile's work for a warp.  YT only decides whether P keeps its low part:
-// with bf16 output P is rounded to fp16 once (at most 2^-11 of each weight,
-// random in sign, against the 2^-8 of the output's own rounding); with fp32
-// output, and for the bf16 cache (where P has to be bf16, 2^-8), P is split into
-// a high and a low part and multiplied twice.
+// One tile's work for a warp.  The weights are p = 2^(x - m) with m the running maximum
+// of a piece's scores (log2 units) less kLift, and l adds them in fp32.  For the
+// product they are rounded:
+//   quantized cache, bf16 output  one fp16 part, off by 2^-11 of each weight, where the
+//                                 output's own rounding is 2^-8.  Two parts: 189 us against
+//                                 170 for 32 x 16,384 tokens of NVFP4 (177 with the low
+//                                 part in the columns that pad G <= 4 to 8), 9.7 against
+//                                 8.7 for 1 x 8,192 of E4M3
+//   quantized cache, fp32 output  two fp16 parts multiplied in turn, 2^-22
+//   BF16 cache                    two bf16 parts, 2^-16
+// fp16 parts also have an absolute step: a weight is off by up to 2^-25 however
+// small it is.  So weights use fp16's range: the row's largest lies between
+// 2^10 and 2^15, and that error is at most 2^-35 of it (with m the maximum
+// itself, all tokens below 2^-25 of a dominant one would be lost, however many).  A
+// lift of 12 would raise m for every rise by 2^3, not 2^5: 16 x 8,192 tokens of E4M3, 64 /
+// 4 heads of 64, 20.4 us against 19.9 (19.7 with 2^8 and none).  bf16 parts have no
+// such step and need no lift.
 template <int FMT, int D, int NT, typename YT>
 struct Warp {
     using C = Cfg<FMT, D, NT>;
     static constexpr bool kBf16 = FMT == NVFP4_KV_BF16;
     static constexpr bool kSplit = kBf16 || std::is_same<YT, float>::value;
+    static constexpr float kLift = kBf16 ? 0.0f : 10.0f, kTop = kBf16 ? 8.0f : 15.0f;
     static constexpr int kUk = C::kDb / 4 < 16 ? C::kDb / 4 : 16;  // bytes of a key row a thread takes at a time
     static constexpr int kNk = C::kDb / (4 * kUk);
     static constexpr int kUv = C::kDb / 8 < 16 ? C::kDb / 8 : 16;  // bytes of a value row
@@ -376,10 +389,14 @@ struct Warp {
         sc[1] = prmt(h, h, 0x3232);
     }
 
-    // Would a score x weigh more than 2^8?  fp16 cannot hold 2^16, so the difference is
-    // rounded as the weight's exponent is: scores from 2^26 on lie 8 and more apart, and
-    // m + 8 may round to m + 16.
-    static NVFP4_DEV bool passes(float x, float m) { return kBf16 ? x > m + 8.0f : x - m > 8.0f; }
+    // Would a score x weigh more than 2^kTop?  fp16 cannot hold 2^16, so the difference is
+    // rounded as the weight's exponent is: scores from 2^26 on lie 8 and more apart.
+    static NVFP4_DEV bool passes(float x, float m) { return kBf16 ? x > m + kTop : x - m > kTop; }
+    // m for a maximum mx; mx itself where the difference rounds to more than kTop.
+    static NVFP4_DEV float lifted(float mx) {
+        const float m = mx - kLift;
+        return mx - m > kTop ? mx : m;
+    }
 
     // kStep tiles with tokens tok0 .. tok0 + 16 kStep - 1 at tp[0], tp[1]; tokens
     // outside [lo, hi) are masked (their bytes may be anything, NaN included).
@@ -408,9 +425,8 @@ struct Warp {
                         if (tok < lo || tok >= hi) x[u][c] = __int_as_float(0xff800000);
                     }
             }
-            // the running maximum is raised only when a score passes it by
-            // more than 2^8 in weight: it only guards the range (weights stay
-            // below 2^8, sums in fp32), so most tiles need no exchange
+            // m is raised only when a weight would pass 2^kTop: most tiles need no
+            // exchange
             float up[2] = {fmaxf(x[0][0], x[0][2]), fmaxf(x[0][1], x[0][3])};
             if constexpr (kStep == 2) {
                 up[0] = fmaxf(up[0], fmaxf(x[1][0], x[1][2]));
@@ -422,7 +438,7 @@ struct Warp {
                     float mx = up[c];
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    mx = fmaxf(mx, m[n][c]);
+                    mx = fmaxf(lifted(mx), m[n][c]);
                     const float al = weight(m[n][c], mx);
                     m[n][c] = mx;
                     l[n][c] *= al;

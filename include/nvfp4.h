@@ -585,8 +585,10 @@ int nvfp4_rope_kv_write(const nvfp4_kv_cache* cache, const void* q, const void* 
  * Numerics: scores, softmax sums and outputs accumulate in fp32.  Quantized
  * caches are multiplied exactly (E2M1 x E4M3 in fp16); queries enter as fp16
  * after a per-head power-of-two prescale (exact for elements within 2^31 of
- * the head's largest).  Softmax weights are rounded to fp16 for bf16 output and
- * carry a second, low part for fp32 output and the BF16 cache.  The result
+ * the head's largest).  Softmax weights are rounded: over quantized caches to
+ * fp16 for bf16 output (2^-11 of each weight), to two fp16 parts for fp32 output
+ * (2^-22), and in either case by up to 2^-35 of the row's largest weight; to two
+ * bf16 parts (2^-16) over the BF16 cache.  The result
  * does not depend on anything but the arguments' shapes and values: the same
  * call gives the same bits.
  * Requires 1 <= B <= 4096, q_heads a multiple of cache->heads, max_pages >= 1,

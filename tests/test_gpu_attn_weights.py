@@ -1,4 +1,6 @@
-"""Decode attention at the ends of the softmax weights' range."""
+"""Decode attention at the ends of the softmax weights' range: scores that fp32 holds in
+coarse steps; one token that takes almost all weight and holds next to nothing (an attention
+sink), and a long tail far below it whose values are the output."""
 import numpy as np
 import pytest
 import torch
@@ -42,3 +44,60 @@ def test_neighbouring_huge_scores(cuda_device, fmt, odd, extra, y_dtype):
     assert_close(y, np.broadcast_to(ref, (B, 2, D)), by, "y")
     top = 16.0 * np.log(2.0) * (14565376.0 + float(k[40, 0, 0]))
     assert np.abs(host(lse) / top - 1).max() <= 2.0 ** -21
+
+
+# The sink's score over the tail's, in nats (2^-17 to 2^-32 in weight).
+DEPTHS = (12.0, 14.25, 15.75, 16.5, 17.25, 18.0, 19.5, 21.75)
+KEY = 0.75                                                       # exact in every format at the scales below
+
+
+def sink_bounds(fmt, D, y, lse, spread, mag, top, v_sum, y_dtype):
+    """Bounds of |y - ref| and of |lse - ref| of one row.  Scores, exponentials and sums as in
+    attn_checks.attn_bounds (D fp32 additions a tensor-core step 2^-23 each of `mag`; 4 * 2^-23 of it and
+    2^-21; fp32 sums over two parts of n / 16 tiles and the joins, 700 at most here).  A weight
+    is rounded: one fp16 part 2^-11 (quantized cache, bf16 output), two fp16 parts 2^-22 (fp32
+    output), two bf16 parts 2^-16.  fp16 is also off by 2^-25 where a weight is small; the row's
+    largest is at least 2^10, so that is 2^-35 of the largest weight `top` for every token."""
+    err = mag * (D + 12) * 2.0 ** -23 + 2.0 ** -21
+    part = 2.0 ** -16 if fmt == oat.BF16 else 2.0 ** -22 if y_dtype == torch.float32 else 2.0 ** -11
+    step = 0.0 if fmt == oat.BF16 else 2.0 ** -35
+    rel = 2 * np.expm1(err) + part + 700 * 2.0 ** -23
+    by = spread * rel[:, None] + step * top[:, None] * v_sum + HALF_STEP[y_dtype] * np.abs(y) + 1e-30
+    return by, 2 * err + 700 * 2.0 ** -23 + 2.0 ** -22 * np.abs(lse)
+
+
+@pytest.mark.parametrize("y_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("G", [2, 6, 16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("fmt", (oat.BF16, oat.E4M3, oat.NVFP4))
+def test_tail_below_a_sink(cuda_device, fmt, D, G, y_dtype):
+    """600 sequences over the same 3,500 rows, so that a warp walks through thousands of them
+    behind the sink; every sequence has its own depth."""
+    n, page, B, Hkv = 3500, 64, 600, 4
+    pages = -(-n // page)
+    rng = np.random.default_rng(5)
+    gs = {oat.BF16: 1.0, oat.E4M3: 1.0 / 64, oat.NVFP4: 1.0 / 512}[fmt]
+    cache = nv.KVCache.empty(pages, page, Hkv, D, FMT[fmt], scalar(gs), scalar(gs))
+    k = np.zeros((n, Hkv, D), np.float32)
+    k[0] = KEY
+    v = (0.5 * rng.standard_normal((n, Hkv, D)) + 0.3).astype(np.float32)
+    v[0] = 0.0
+    slots = dev(np.arange(n))
+    nv.nvfp4_kv_write(cache, dev(k), dev(v), slots)
+    kr, vr = (host(x) for x in nv.nvfp4_kv_read(cache, slots, y_dtype=torch.float32))
+    assert np.array_equal(kr, k) and not vr[0].any()
+    # scale q . k_0 = depth at scale 1 / D (16 .. 29: exact in bf16)
+    depth = np.array([DEPTHS[b % len(DEPTHS)] for b in range(B)], np.float32)
+    q = torch.from_numpy(depth / np.float32(KEY)).to(torch.bfloat16)[:, None, None].expand(B, Hkv * G, D).contiguous().cuda()
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(B, pages).contiguous()
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    y, lse = nv.nvfp4_attn_decode(q, cache, table, lens, scale=1.0 / D, want_lse=True, y_dtype=y_dtype)
+    for i in range(len(DEPTHS)):
+        ry, rl, spread, mag = oat.attend(host(q[i]), kr, vr, 1.0 / D)
+        top = np.exp(DEPTHS[i] - rl)
+        v_sum = np.abs(vr).sum(0).repeat(G, 0)
+        by, bl = sink_bounds(fmt, D, ry, rl, spread, mag, top, v_sum, y_dtype)
+        for b in range(i, B, len(DEPTHS)):
+            assert_close(y[b], ry, by, f"y[{b}], {DEPTHS[i]} nats")
+            assert_close(lse[b], rl, bl, f"lse[{b}], {DEPTHS[i]} nats")
+    assert nv.nvfp4_read_device_status() == nv.OK
