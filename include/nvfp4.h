@@ -588,7 +588,9 @@ int nvfp4_rope_kv_write(const nvfp4_kv_cache* cache, const void* q, const void* 
  * the head's largest).  Softmax weights are rounded: over quantized caches to
  * fp16 for bf16 output (2^-11 of each weight), to two fp16 parts for fp32 output
  * (2^-22), and in either case by up to 2^-35 of the row's largest weight; to two
- * bf16 parts (2^-16) over the BF16 cache.  The result
+ * bf16 parts (2^-16) over the BF16 cache.  The sums behind an output are fp32
+ * and up to 2^15 times the seen tokens larger than it, so v_gs may be up to 2^70
+ * here.  The result
  * does not depend on anything but the arguments' shapes and values: the same
  * call gives the same bits.
  * Requires 1 <= B <= 4096, q_heads a multiple of cache->heads, max_pages >= 1,

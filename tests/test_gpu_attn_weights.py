@@ -101,3 +101,28 @@ def test_tail_below_a_sink(cuda_device, fmt, D, G, y_dtype):
             assert_close(y[b], ry, by, f"y[{b}], {DEPTHS[i]} nats")
             assert_close(lse[b], rl, bl, f"lse[{b}], {DEPTHS[i]} nats")
     assert nv.nvfp4_read_device_status() == nv.OK
+
+
+@pytest.mark.parametrize("y_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,extra", [(1, 0), (1, 2400), (400, 0), (400, 1200)])
+@pytest.mark.parametrize("fmt,v_gs", [(oat.E4M3, 2.0 ** 70), (oat.E4M3, 2.0 ** -110), (oat.NVFP4, 2.0 ** 70),
+                                      (oat.NVFP4, 2.0 ** -110)])
+def test_large_and_small_value_scales(cuda_device, fmt, v_gs, B, extra, y_dtype):
+    """The same values (powers of two from 1/16 to 256 before the scale) at scales that are powers of
+    two: the outputs are those at scale 1 times the scale, to the bit."""
+    D, page, n = 128, 16, 1024
+    rng = np.random.default_rng(8)
+    k = rng.standard_normal((n, 1, D)).astype(np.float32)
+    v = np.exp2(rng.integers(-4, 9, (n, 1, D))).astype(np.float32)
+    q = torch.from_numpy(rng.standard_normal((B, 3, D)).astype(np.float32)).to(torch.bfloat16).cuda()
+    table = torch.cat((torch.arange(n // page), torch.zeros(extra))).int().cuda().expand(B, -1).contiguous()
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    slots = dev(np.arange(n))
+    out = []
+    for gs in (1.0, v_gs):
+        cache = nv.KVCache.empty(n // page, page, 1, D, FMT[fmt], scalar(0.02), scalar(1.0))
+        nv.nvfp4_kv_write(cache, dev(k), dev(v), slots)
+        cache = nv.KVCache(cache.data, page, 1, D, FMT[fmt], cache.k_gs, scalar(gs))
+        out.append(nv.nvfp4_attn_decode(q, cache, table, lens, y_dtype=y_dtype))
+    # (outputs lie above 2^-4 of a scale, far from the ends of fp32, and so do the sums behind them)
+    assert torch.equal(out[1], out[0] * v_gs)
