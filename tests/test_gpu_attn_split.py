@@ -83,3 +83,28 @@ def test_captured_graphs_share_a_workspace(cuda_device, split):
 
 def test_two_streams_at_once(cuda_device, split):
     cases.test_two_streams_at_once(cuda_device, COLS)
+
+
+# ---- windows: the list counts the seen tiles only, from a first one inside the sequence ----
+
+@pytest.mark.parametrize("y_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt,D,page", [(oat.NVFP4, 128, 48), (oat.NVFP4, 64, 256), (oat.E4M3, 128, 16),
+                                        (oat.BF16, 256, 64)])
+def test_long_window(cuda_device, split, fmt, D, page, y_dtype):
+    """Windows that begin inside a tile, a sequence inside its window and an empty one."""
+    b = cases.Batch(fmt, D, 2, 2, page, (30_011, 25_000, 0, 17))
+    for window in (20_003, 16_900):
+        b.check(*b.run(window=window, y_dtype=y_dtype), window=window)
+
+
+@pytest.mark.parametrize("y_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt,D", [(oat.NVFP4, 128), (oat.NVFP4, 256), (oat.E4M3, 64), (oat.BF16, 128)])
+def test_window_over_many_sequences(cuda_device, split, fmt, D, y_dtype):
+    """Segments that begin and end anywhere in a warp's range, each from another first tile."""
+    lens = [int(x) for x in np.random.default_rng(6).integers(0, 4500, 64)]
+    lens[:4] = 0, 1, 2_601, 4_499
+    b = cases.Batch(fmt, D, 5, 2, 32, lens)
+    y, lse = b.run(window=2_600, y_dtype=y_dtype)
+    b.check(y, lse, window=2_600, seqs=list(range(0, 64, 5)) + [1, 2, 3, 63])
+    y2, lse2 = b.run(window=2_600, y_dtype=y_dtype)
+    assert torch.equal(y, y2) and torch.equal(lse, lse2)         # the same bits
