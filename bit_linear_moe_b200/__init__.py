@@ -454,7 +454,24 @@ def _cuda(t: torch.Tensor, what: str) -> torch.device:
 class KVCache:
     """A paged key-value cache: the device memory ``data`` (uint8, contiguous, a whole
     number of pages) with its shape, format and the fp32 global scales of the keys
-    and values (one-element tensors; not used by ``KV_BF16``)."""
+    and values (one-element tensors; not used by ``KV_BF16``).
+
+    The calls use the tensors given here, which the object keeps alive: its attributes
+    cannot be set again.  New values are copied into the tensors (``cache.k_gs.copy_``);
+    other tensors make another ``KVCache``."""
+
+    _FIXED = frozenset(("data", "k_gs", "v_gs", "num_pages", "page_size", "heads", "head_dim", "format", "device",
+                        "_desc", "_ref"))
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED and name in self.__dict__:
+            raise AttributeError(f"{name} of a KVCache cannot be set: its calls use what it was made with")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        if name in self._FIXED:
+            raise AttributeError(f"{name} of a KVCache cannot be deleted: its calls use what it was made with")
+        object.__delattr__(self, name)
 
     def __init__(self, data: torch.Tensor, page_size: int, heads: int, head_dim: int, format: int, k_gs=None,
                  v_gs=None):
