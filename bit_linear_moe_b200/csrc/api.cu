@@ -673,9 +673,12 @@ int nvfp4_rope_freqs(int32_t rot_dim, double theta, int scaling, double factor, 
         return NVFP4_ERR_SHAPE;
     if (scaling != NVFP4_ROPE_SCALE_NONE && !(factor >= 1.0 && isfinite(factor))) return NVFP4_ERR_SHAPE;
     if (scaling == NVFP4_ROPE_SCALE_NTK && rot_dim < 4) return NVFP4_ERR_SHAPE;
-    if (scaling == NVFP4_ROPE_SCALE_YARN && (!(original_len >= 1.0) || !(beta_fast > beta_slow)))
+    if (scaling == NVFP4_ROPE_SCALE_YARN &&
+        (!(original_len >= 1.0 && isfinite(original_len)) || !(beta_fast > beta_slow && isfinite(beta_fast - beta_slow))))
         return NVFP4_ERR_SHAPE;
     if (scaling == NVFP4_ROPE_SCALE_NTK) theta *= pow(factor, (double)rot_dim / (rot_dim - 2));
+    // the last pair turns fastest (a small base) or slowest
+    if (!isfinite(theta) || !isfinite(pow(theta, -(rot_dim - 2.0) / rot_dim))) return NVFP4_ERR_SHAPE;
     for (int i = 0; i < rot_dim / 2; ++i) {
         double f = pow(theta, -2.0 * i / rot_dim) / 6.283185307179586476925;
         if (scaling == NVFP4_ROPE_SCALE_LINEAR) f /= factor;

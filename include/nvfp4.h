@@ -473,7 +473,8 @@ int moe_grouped_linear_w4a4_ws_layout(int64_t R, int64_t K, int64_t N, int32_t E
  * and *mscale_out with the magnitude (1 but for YARN).  Copy freqs to the
  * device for the calls below.  Requires rot_dim % 2 == 0, 2 <= rot_dim <=
  * 1024 (NTK: rot_dim >= 4), finite theta > 0, and, where they are used, finite
- * factor >= 1, original_len >= 1, beta_fast > beta_slow; ERR_SHAPE otherwise. */
+ * factor >= 1, original_len >= 1 and beta_fast > beta_slow; NTK's base and every
+ * frequency must be finite too; ERR_SHAPE otherwise. */
 int nvfp4_rope_freqs(int32_t rot_dim, double theta, int scaling, double factor, double original_len,
                      double beta_fast, double beta_slow, double* freqs, double* mscale_out);
 
