@@ -418,13 +418,6 @@ NVFP4_DEV constexpr int value_scales() {
     return kKvTile * (kv_scale_bytes(FMT, D) - kv_code_bytes(FMT, D));
 }
 
-NVFP4_DEV float amax8(const float (&v)[8]) {
-    float m = fabsf(v[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-    return m;
-}
-
 struct KvWriteArgs {
     KvView c;
     const void* q;  // ROPE: [T] rows of q_heads heads

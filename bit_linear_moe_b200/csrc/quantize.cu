@@ -23,13 +23,6 @@
 
 namespace nvfp4 {
 
-NVFP4_DEV float amax8(const float (&v)[8]) {
-    float m = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
-    return m;
-}
-
 NVFP4_DEV void block_amax_to(float m, unsigned* amax_bits) {
     m = warp_max(m);
     __shared__ float red[8];

@@ -1,6 +1,6 @@
 // Quantizer pieces shared by the kernels that write NVFP4 (quantize.cu) and
-// the key-value cache (kv_cache.cu): vector loads to fp32 and E4M3 / E2M1
-// codes of IEEE round-to-nearest quotients.
+// the key-value cache (kv_cache.cu): vector loads to fp32, magnitudes, and
+// E4M3 / E2M1 codes of IEEE round-to-nearest quotients.
 #pragma once
 
 #include "common.cuh"
@@ -49,6 +49,14 @@ NVFP4_DEV void load16(const T* p, float (&v)[16]) {
         v[j] = a[j];
         v[8 + j] = b[j];
     }
+}
+
+// Largest magnitude (0 where all are NaN).
+NVFP4_DEV float amax8(const float (&v)[8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+    return m;
 }
 
 // Approximate reciprocal (relative error below 2^-22 for normal inputs).
