@@ -523,7 +523,8 @@ def nvfp4_rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, la
                mscale: float = 1.0, inverse: bool = False, y=None, y_dtype=torch.bfloat16):
     """Rotary positions of ``x [T, heads, head_dim]`` (fp32 or bf16; a view of wider rows
     is read in place).  ``positions [T]`` int64, ``freqs`` from :func:`nvfp4_rope_freqs`
-    on x's device.  ``y=x`` rotates in place."""
+    on x's device.  ``y=x`` rotates in place.  Like the other calls it records nothing for
+    autograd; ``inverse=True`` on a gradient of ``y`` is the gradient of ``x``."""
     dev = _cuda(x, "x")
     x_ld = _heads_view(x, dev, "x")
     T, heads, D = x.shape
@@ -602,7 +603,8 @@ def nvfp4_attn_decode(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     """Attention of one new token per sequence: ``q [B, q_heads, head_dim]`` (bf16 view)
     over the paged cache.  ``page_table [B, max_pages]`` and ``seq_lens [B]`` int32;
     ``scale`` defaults to ``head_dim ** -0.5``.  Returns ``y [B, q_heads, head_dim]``,
-    or ``(y, lse [B, q_heads])``."""
+    or ``(y, lse [B, q_heads])``.  Short batches are faster with a narrow table (a slice
+    ``table[:, :n]`` is taken in place): the work is split by its width."""
     dev = cache.device
     B, q_heads, D = q.shape[0], q.shape[1], cache.head_dim
     q_ld = _heads_view(q, dev, "q", B, q_heads, D)

@@ -15,8 +15,11 @@ struct Plan {
     size_t header, bytes;
 };
 
-// The grid: two CTAs per SM, fewer when even the longest sequences leave no
-// tile for each warp.  False for shapes out of range.
+// The grid: two CTAs per SM (one where a tile is 16 KB), fewer when even the longest
+// sequences leave no tile for each warp.  The list takes 8 bytes of a CTA's shared
+// memory per sequence, so beyond some 940 sequences (NVFP4, heads of 128) one CTA fits an
+// SM and the grid runs in two waves: 1,024-token contexts, 16 / 8 heads, 900 sequences
+// 238 us (4.5 TB/s), 1,024 sequences 360 us (3.4 TB/s).  False for shapes out of range.
 static bool plan(const KvView& c, int64_t B, int q_heads, int64_t max_pages, Plan& p) {
     if (B < 1 || B > 4096 || q_heads < 1 || q_heads % c.heads || max_pages < 1 || max_pages > 0x7fffffff) return false;
     p.G = q_heads / c.heads;

@@ -36,15 +36,20 @@
 //
 // Measured (B200, replayed from a graph; floor: the bytes at 6,566 GB/s):
 //   32 ragged sequences of up to 16,384 tokens, 40 query / 20 key heads, NVFP4:
-//     169 us, 4.6 TB/s, 70 % of the floor.  Copies alone (no products) take 129;
-//     without the values' half 144, without the scores' 150 (of 190, then): what
-//     bounds it is issuing the conversions and fragments of both products.
+//     170 us, 4.6 TB/s, 69 % of the floor.  Copies alone (no products) take 129;
+//     without the values' half 144, without the scores' 150 (of 190, then).  Both
+//     products' conversions and fragments count, but the issue slots are 62 % used (8 x
+//     8,192 tokens) and DRAM less than half: a warp's scores, softmax and values follow
+//     one another, and four warps per scheduler do not cover their latencies.
 //   1 x 131,071, 32 / 8 heads, E4M3: 53 us, 5.1 TB/s, 78 %; copies alone 50
-//     (about 9 us of it before the first bytes and in the join).
-//   1 x 8,192, 40 / 20 heads, NVFP4: 13.2 us (segment kernel), latency: 8 tiles
+//     (about 9 us of it before the first bytes and in the join).  fp32 output: 53 us;
+//     of the batch above 189.
+//   1 x 8,192, 40 / 20 heads, NVFP4: 12.8 us (segment kernel), latency: 8 tiles
 //     one after the other per warp, launch, page table and two joins.
-//   64 ragged x 2,048, 32 / 2 heads of 64, BF16: 14.5 us; 16 x 4,000 with a
-//     window of 1,000, 16 / 8 heads of 256, NVFP4: 13.5 us; 1 x 97: 4.2 us.
+//   64 ragged x 2,048, 32 / 2 heads of 64, BF16: 14.1 us; 16 x 4,000 with a
+//     window of 1,000, 16 / 8 heads of 256, NVFP4: 13.2 us; 1 x 97: 4.0 us.
+//   The same with a page table of 131,072 tokens (even split and join): 1 x 8,192
+//     16.3 us, 64 x 2,048 21.8, 1 x 97 8.4; the others as above.
 // Slower, measured on the first of these: the scores on the block-scaled
 // tcgen05 MMA, queries as six NVFP4 terms (344 us; 382 with separate roles: a
 // tile's 16 rows fill an eighth of an MMA), codes unpacked by bit operations (217
@@ -95,7 +100,9 @@ struct Shape {
 // (16) 21.8 / 21.9, 16 x 4,096 (32) 36.0 / 35.3, 1 x 32,768 (32) 38.4 / 32.5; 8 heads of
 // 256: 1 x 4,096 (8) 10.9 / 12.7, 1 x 8,192 (16) 16.1 / 15.0; E4M3, 8 heads of 128: 4 x
 // 16,384 (16) 19.9 / 24.4, 1 x 32,768 (32) 23.6 / 23.2; BF16, 8 heads of 128: 4 x 4,096
-// (8) 10.9 / 14.2, 1 x 16,384 (32) 24.5 / 22.5.
+// (8) 10.9 / 14.2, 1 x 16,384 (32) 24.5 / 22.5.  At 16 tiles neither is always the faster.
+// Segments beyond the resident CTAs run in waves: 8 heads of 128, NVFP4, 512 x 1,024 tokens (8)
+// 148 / 143, 900 x 1,024 (8) 255 / 238, 4,096 x 256 (2) 525 / 407.
 constexpr int64_t kSegmentTiles = 16;
 // What beginning and ending a segment costs a warp, in tiles (measured: 2 x
 // the 2,000 cycles of an NVFP4 tile at D = 128).
@@ -118,9 +125,9 @@ struct Cfg {
     static constexpr int kTile = kv_tile_bytes(FMT, D);
     static constexpr int kPieces = kDb / 16;
     static constexpr int kWarps = (D == 256 || kTile >= 8192 || (D == 128 && NT == 2)) ? 4 : 8;
-    // ring: about 72 KB per CTA, so that two CTAs fit an SM and some 140 KB
-    // are on their way per SM (44 bytes per ns times ~1 us of loaded latency
-    // asks for at least 44 KB)
+    // ring: about 72 KB per CTA, so that two CTAs fit an SM (with the list of up to some
+    // 940 sequences) and some 140 KB are on their way per SM (44 bytes per ns times
+    // ~1 us of loaded latency asks for at least 44 KB)
     static constexpr int kRing = kTile >= 16384 ? 2 : (72 * 1024) / (kWarps * kTile) > 8 ? 8 : (72 * 1024) / (kWarps * kTile);
     static constexpr int kRingBytes = kWarps * kRing * kTile;
     static constexpr int kPieceBytes = Piece<D, NT>::kFloats * 4;

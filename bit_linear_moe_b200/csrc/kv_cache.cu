@@ -27,12 +27,19 @@
 // instruction.  All are programmatic dependents.
 //
 // Measured (B200, replayed from a graph):
-//   rotation of 8,191 tokens x 40 heads of 128, 64 rotated, bf16: 27.6 us, 6.1 TB/s
-//     (92 % of a copy's rate); one token: 1.9 us, the launch
+//   rotation of 8,191 tokens x 40 heads of 128, 64 rotated, bf16: 27.3 us, 6.1 TB/s
+//     (94 % of a copy's rate); one token: 1.9 us, the launch
 //   2,048 tokens of 20 heads written to NVFP4 pages and 10,240 read back: 33.1 us,
-//     4.9 TB/s (74 %).  The write is what is slow (11.7 us alone, 4.1 of it bytes):
-//     some 19 instructions an element and two waves of CTAs, each with the latency of
-//     its first loads
+//     4.9 TB/s (74 %).  The write is what is slow (12.0 us alone, 4.1 of it bytes).  Half
+//     is instructions (19 an element, 6.8 M of warps), half the grid: 768 CTAs are 1.3
+//     waves of the 592 resident ones, the last of three groups of heads is half empty,
+//     and each wave begins with the latency of its loads (56 % of the issue slots)
+//   2,048 tokens, bf16 / fp32 rows, to BF16, E4M3 and NVFP4 pages: write of 2 x 20 heads 8.3
+//     / 11.4, 9.8 / 10.6 and 12.0 / 11.1 us; rotation and write of 40 + 2 x 20 14.7 / 22.2,
+//     18.2 / 24.3 and 22.8 / 26.7; the latter of 32 tokens, fp32 rows, 3.1, 3.5 and 4.0.
+//     Read of 10,240 tokens of 20 heads 34.2, 26.8 and 24.1 us (94, 89 and 85 %).  The
+//     global scales are those of the data's largest elements; where fewer quotients meet
+//     a border between codes the NVFP4 write takes 9.1 us, with the rotation 19.4
 //   rotation, write and read of 2,048 tokens, 32 / 8 heads, bf16: 14.8 us, 4.5 TB/s
 //     (69 %): two short kernels, each with its ramp; 32 decoding tokens: 5.6 us
 #include "internal.h"
@@ -693,7 +700,9 @@ __global__ void __launch_bounds__(kCtaThreads, 6) kv_read_kernel(const KvReadArg
 // 8,191 x 40 heads with 4 / 8 / 16 per SM 28.2 / 27.5 / 28.3 (four rows per lane, 4:
 // 28.8); rotation and write of 2,048 x (40 + 2 x 20) heads, NVFP4, with 4 / 8: 23.0 /
 // 24.6 (four rows, 4: 32.9), 32 + 2 x 8 heads, bf16: 11.3 / 12.8; write of 2,048 x 2 x
-// 20 heads, NVFP4, with 4 / 16: 11.7 / 12.5; read of them 6.1 / 5.5.
+// 20 heads, NVFP4, with 4 / 16: 11.7 / 12.5; read of them 6.1 / 5.5.  Doubling hc leaves
+// uneven grids: 1.3 waves (1.7 of the three CTAs per SM of fp32 rows) for 2,048
+// tokens and 40, 48 or 80 heads.
 static void cta_shape(int64_t T, int heads, int units, int per_sm, int& tt, int& hc) {
     const int per = units < 32 ? 32 / units : 1;
     tt = per;

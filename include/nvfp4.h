@@ -469,7 +469,12 @@ int moe_grouped_linear_w4a4_ws_layout(int64_t R, int64_t K, int64_t N, int32_t E
  *             beta_slow) / (beta_fast - beta_slow), 0, 1): pairs that turn
  *             beta_fast times or more within original_len keep their
  *             frequency, those that turn beta_slow times or less are
- *             interpolated; cos and sin get the magnitude 0.1 ln(factor) + 1
+ *             interpolated; cos and sin get the magnitude 0.1 ln(factor) + 1.
+ *             The ramp is linear in turns, as the method's paper defines it.
+ *             Code that ramps linearly in the pair index between two rounded
+ *             bounds gives other frequencies there (up to 42 % apart at rot_dim 128,
+ *             theta 1e6, factor 4, original_len 32,768): for a model tuned with
+ *             those, fill freqs with them
  * and *mscale_out with the magnitude (1 but for YARN).  Copy freqs to the
  * device for the calls below.  Requires rot_dim % 2 == 0, 2 <= rot_dim <=
  * 1024 (NTK: rot_dim >= 4), finite theta > 0, and, where they are used, finite
@@ -485,7 +490,7 @@ int nvfp4_rope_freqs(int32_t rot_dim, double theta, int scaling, double factor, 
  *   HALF         u = x[i],  v = x[i + rot_dim / 2]
  *   INTERLEAVED  u = x[2i], v = x[2i + 1]
  * and elements rot_dim .. head_dim - 1 pass through; y is rounded to y_dtype.
- * inverse != 0 turns back (-a; also the gradient's rotation).
+ * inverse != 0 turns back (-a): with a gradient of y as x, the gradient of x.
  *   x          [T] rows at stride x_ld elements, each `heads` heads of
  *              head_dim (a column slice of the QKV output is read in place)
  *   positions  [T] int64, of magnitude below 2^53 (negative ones turn back)
@@ -583,6 +588,14 @@ int nvfp4_rope_kv_write(const nvfp4_kv_cache* cache, const void* q, const void* 
  * A page index out of range, or a length above max_pages * page_size, is
  * reported as NVFP4_ERR_PAGE in the device status word; that sequence's output
  * is then unspecified (nothing out of range is read).
+ * The host does not read seq_lens, so the work is split by what max_pages (or the
+ * window) allows, not by what the lengths are.  Where that is at most 16 tiles of 16
+ * tokens for each warp of a cluster of CTAs per (sequence, key head), one kernel
+ * does all; beyond, a kernel splits the seen tiles of the whole batch evenly and
+ * a second one joins.  For short sequences the second way is slower (1 x 97
+ * tokens 8.4 us against 4.0, 1 x 8,192 16.3 against 12.8, 64 x 2,048 21.8 against 14.1),
+ * so pass the leading columns of a wide table that the batch needs; long batches
+ * and windows do not depend on the width.
  * Numerics: scores, softmax sums and outputs accumulate in fp32.  Quantized
  * caches are multiplied exactly (E2M1 x E4M3 in fp16); queries enter as fp16
  * after a per-head power-of-two prescale (exact for elements within 2^31 of
@@ -591,9 +604,8 @@ int nvfp4_rope_kv_write(const nvfp4_kv_cache* cache, const void* q, const void* 
  * (2^-22), and in either case by up to 2^-35 of the row's largest weight; to two
  * bf16 parts (2^-16) over the BF16 cache.  The sums behind an output are fp32
  * and up to 2^15 times the seen tokens larger than it, so v_gs may be up to 2^70
- * here.  The result
- * does not depend on anything but the arguments' shapes and values: the same
- * call gives the same bits.
+ * here.  The result does not depend on anything but the arguments' shapes and
+ * values: the same call gives the same bits.
  * Requires 1 <= B <= 4096, q_heads a multiple of cache->heads, max_pages >= 1,
  * B * heads * ceil(q_heads / heads / 8) * (max_pages * page_size / 16 + 2) below
  * 2^31, max_pages * page_size below 2^31 - 64, q and y 16-byte aligned,
